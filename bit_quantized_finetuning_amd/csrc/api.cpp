@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "qlora.h"
+#include "host.h"
 #include "kernels.h"
 
 using namespace qlora;
@@ -80,14 +81,7 @@ bool literals_match() {
   return ok;
 }
 
-// Per-tile buffer ranges stay below 2^31 bytes with these bounds.
-constexpr int64_t kMaxDim = (int64_t)1 << 20;
-constexpr int64_t kMaxTokens = (int64_t)1 << 24;
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+// Per-tile buffer ranges stay below 2^31 bytes with kMaxDim and kMaxTokens (host.h).
 
 int validate_weight(const qlora_nf4_weight *W) {
   if (!literals_match()) return QLORA_ERR_INTERNAL;
@@ -101,14 +95,6 @@ int validate_weight(const qlora_nf4_weight *W) {
   if (!W->qscale && W->d_out * W->d_in / QLORA_BLOCK * 4 >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
   if (!aligned16(W->codes) || (W->qscale && !aligned16(W->qscale)) || !aligned16(W->smax)) return QLORA_ERR_ALIGN;
   return QLORA_OK;
-}
-
-int rank_pad(int r) { return r > 0 ? (int)ceil_div(r, 16) * 16 : 0; }
-
-int lora_small_ksplit(int64_t T, int64_t K) {
-  if (T > 64) return 1;
-  int64_t ks = ceil_div(K, 32) / 8;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ks, 64));
 }
 
 // Workspace regions (byte offsets). The counter region is fixed (kMaxCounters
@@ -155,13 +141,6 @@ Layout layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   L.total = off;
   return L;
 }
-
-template <typename T>
-T *at(void *ws, size_t off) {
-  return reinterpret_cast<T *>(static_cast<uint8_t *>(ws) + off);
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
 
 }  // namespace
 

@@ -184,4 +184,68 @@ int lora_grad_ksplit(int64_t M, int64_t N, int64_t T);
 size_t lora_grad_partial_floats(int64_t M, int64_t N, int64_t T);
 int lora_grad_tiles(int64_t M, int64_t N);
 
+// fp8_quant.hip: rows [T, d] (d % 8 == 0) to 8 bits in groups of 128 with power-of-two scales [T, ceil(d / 128)];
+// a weight [N, K] (K % 8 == 0) to e4m3 in blocks of 128 x 128 with scales [ceil(N / 128), ceil(K / 128)].
+hipError_t launch_fp8_quantize_rows(const void *x, bool bf16_in, int64_t T, int64_t d, bool e5m2, uint8_t *codes,
+                                    float *scales, hipStream_t st);
+hipError_t launch_fp8_quantize_weight(const void *W, bool bf16_in, int64_t N, int64_t K, uint8_t *codes, float *scales,
+                                      hipStream_t st);
+
+// fp8_gemm.hip: out[T, N] = the block-scaled product of xq [T, K] with the e4m3 weight [d_out, d_in] (trans false:
+// N = d_out, K = d_in; true: the weight read by columns, N = d_in, K = d_out) + su L^T (su bf16 [T, rp], L bf16
+// [N, r]; r may be 0).
+hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, bool trans,
+                              const uint8_t *xq, const float *xs, bool e5m2, int64_t T, const uint16_t *su, int rp,
+                              const uint16_t *L, int r, uint16_t *out, hipStream_t st);
+
+// rmsnorm.hip: row strides in elements; s, y, yq, dx and the partial sums are dense. partial: rmsnorm_partial_floats
+// floats when dw is wanted, else null.
+struct NormFwd {
+  const void *x, *res, *w;
+  int64_t ldx, ldr;
+  void *s, *y;
+  uint8_t *yq;
+  float *ys, *rstd;
+  int64_t T;
+  int d;
+  float eps;
+  bool w_bf16, e5m2;
+};
+struct NormBwd {
+  const void *dy, *s, *ds, *w;
+  int64_t ldy, lds, ldd;
+  const float *rstd;
+  void *dx;
+  float *partial;
+  int64_t T;
+  int d;
+  bool w_bf16;
+};
+hipError_t launch_rmsnorm_fwd(const NormFwd &a, bool bf16, hipStream_t st);
+hipError_t launch_rmsnorm_bwd(const NormBwd &a, bool bf16, float *dw, hipStream_t st);
+size_t rmsnorm_partial_floats(int64_t T, int64_t d);
+hipError_t launch_fill_f32(float *p, int64_t n, float v, hipStream_t st);
+
+// adamw_many.hip: up to kManyJobs tensors per launch, passed by value as a kernel argument. Tensor j's blocks of 256
+// are blk0[j] .. blk0[j + 1] - 1 of the launch; base is the first one's place in the state arrays.
+constexpr int kManyJobs = 128;
+constexpr int kManyPartials = 1024;  // workgroups of one launch of the norm's pass
+struct ManyJobs {
+  const void *grad[kManyJobs];
+  void *param[kManyJobs];
+  int64_t n[kManyJobs];
+  uint32_t blk0[kManyJobs + 1];
+  int count;
+};
+struct ManyState {
+  void *m, *v;
+  float *m_scale, *v_scale, *master;
+  int64_t base;
+};
+static_assert(sizeof(ManyJobs) + sizeof(ManyState) + sizeof(AdamWArgs) + 16 <= 4096, "kernel arguments");
+hipError_t launch_grad_sq(const ManyJobs &jobs, bool bf16, double *partial, int *wgs, hipStream_t st);
+hipError_t launch_grad_norm(const double *partial, int n, float max_norm, float *norm, float *coef, hipStream_t st);
+hipError_t launch_adamw_many(const ManyJobs &jobs, const ManyState &s, bool grad_bf16, bool bits8, bool master,
+                             const AdamWArgs &a, const float *coef, uint32_t key, hipStream_t st);
+
 }  // namespace qlora

@@ -9,7 +9,9 @@ Function names follow the C ABI in include/qlora.h:
     qlora_quantize, qlora_dequantize, qlora_merge, qlora_forward, qlora_forward_noalloc, qlora_backward,
     qlora_adamw_step, qlora_adamw_step_host, qlora_workspace_fallbacks, qlora_workspace_set_wait_limit, qlora_storage_bytes,
     qlora_storage_bytes_absmax,
-    qlora_workspace_bytes, qlora_nf4_codebook, qlora_nf4_thresholds, qlora_status_string
+    qlora_workspace_bytes, qlora_nf4_codebook, qlora_nf4_thresholds, qlora_status_string,
+    qlora_fp8_quantize, qlora_fp8_quantize_rows, qlora_fp8_forward, qlora_fp8_backward, qlora_fp8_storage_bytes,
+    qlora_fp8_workspace_bytes, qlora_rmsnorm_forward, qlora_rmsnorm_backward, qlora_adamw_many
 
 The C ABI sees only pointers, so every tensor argument is checked here before the call: its shape against the
 weight and the other operands, its dtype, contiguity, and that it lives on the weight's GPU. A mismatch raises
@@ -18,9 +20,11 @@ TypeError (dtype) or ValueError (shape, layout, device) and nothing is launched.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -97,6 +101,41 @@ _lib.qlora_nf4_thresholds.argtypes = [ctypes.POINTER(ctypes.c_float)]
 _lib.qlora_nf4_thresholds.restype = None
 _lib.qlora_status_string.argtypes = [ctypes.c_int]
 _lib.qlora_status_string.restype = ctypes.c_char_p
+
+class _Fp8Weight(ctypes.Structure):
+    _fields_ = [("d_out", _i64), ("d_in", _i64), ("codes", _vp), ("scales", _vp)]
+
+
+class _AdamWJob(ctypes.Structure):
+    _fields_ = [("grad", _vp), ("param", _vp), ("n", _i64)]
+
+
+class _AdamWManyHparams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_double) for k in ("lr", "beta1", "beta2", "eps", "weight_decay")]
+
+
+class _AdamWState(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp), ("master", _vp)]
+
+
+for _name, _args, _res in (
+        ("qlora_fp8_quantize", [_vp, ctypes.c_int, ctypes.POINTER(_Fp8Weight), _vp], ctypes.c_int),
+        ("qlora_fp8_quantize_rows", [_vp, ctypes.c_int, _i64, _i64, ctypes.c_int, _vp, _vp, _vp], ctypes.c_int),
+        ("qlora_fp8_storage_bytes", [_i64, _i64], _sz),
+        ("qlora_fp8_workspace_bytes", [_i64, _i64, _i64, _i32], _sz),
+        ("qlora_fp8_forward", [ctypes.POINTER(_Fp8Weight), _vp, _vp, ctypes.c_int, _vp, _i64, _vp, _vp, _i32, _f32, _vp,
+                               _vp, _vp, _sz, _vp], ctypes.c_int),
+        ("qlora_fp8_backward", [ctypes.POINTER(_Fp8Weight), _vp, _vp, ctypes.c_int, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
+                                _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+        ("qlora_rmsnorm_forward", [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int, _f32, _vp, _vp, _vp,
+                                   _vp, ctypes.c_int, _vp, _vp], ctypes.c_int),
+        ("qlora_rmsnorm_workspace_bytes", [_i64, _i64], _sz),
+        ("qlora_rmsnorm_backward", [_vp, _i64, _vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int, _vp, _vp,
+                                    _vp, _vp, _sz, _vp], ctypes.c_int),
+        ("qlora_adamw_many_workspace_bytes", [_i32], _sz),
+        ("qlora_adamw_many", [_vp, _i64, ctypes.POINTER(_AdamWJob), _i32, ctypes.c_int, ctypes.c_int,
+                              ctypes.POINTER(_AdamWState), _f32, _vp, ctypes.c_uint32, _vp, _sz, _vp], ctypes.c_int)):
+    getattr(_lib, _name).argtypes, getattr(_lib, _name).restype = _args, _res
 
 lib = _lib  # raw handle, for tests of the C ABI itself
 
@@ -618,3 +657,419 @@ def qlora_backward(w: NF4Weight, x: torch.Tensor | None, dY: torch.Tensor, A: to
     _check(_lib.qlora_backward(ctypes.byref(cw), _ptr(x), _ptr(dY), T, _ptr(A), _ptr(B), r, alpha, _ptr(u_saved),
                                _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(dev)), "qlora_backward")
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit frozen base
+# ---------------------------------------------------------------------------
+
+FP8_GROUP = 128     # QLORA_FP8_GROUP
+ADAMW_BLOCK = 256   # QLORA_ADAMW_BLOCK
+NORM_MAX_DIM = 32768  # QLORA_NORM_MAX_DIM
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+_FMT = {E4M3: 2, E5M2: 3}
+_FLOAT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _fmt(fmt) -> int:
+    if fmt not in _FMT:
+        raise TypeError(f"fmt must be torch.float8_e4m3fn or torch.float8_e5m2, got {fmt}")
+    return _FMT[fmt]
+
+
+def _float(t, name: str) -> int:
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in _FLOAT:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return _FLOAT[t.dtype]
+
+
+def _groups(d: int) -> int:
+    return -(-d // FP8_GROUP)
+
+
+def _on(dev):
+    """The library launches on the current device: make `dev` current where it is not."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _call_ws(dev, nbytes: int, ws, counters: bool = True):
+    """The caller's workspace, or the device's cached one. A call that is being captured into a graph gets one of
+    its own from the graph's memory pool (with its counters cleared by a kernel of the graph), so that replays
+    share nothing with eager calls or other graphs."""
+    if ws is not None:
+        return _own_workspace(ws, nbytes)
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if counters:
+            ws[:COUNTER_BYTES].zero_()
+        return ws
+    return workspace(dev, nbytes)
+
+
+@dataclass
+class Fp8Weight:
+    """A frozen weight in e4m3 with one float32 scale per 128 x 128 block: the buffers of qlora_fp8_weight."""
+    d_out: int
+    d_in: int
+    codes: torch.Tensor   # float8_e4m3fn [d_out, d_in]
+    scales: torch.Tensor  # float32 [ceil(d_out / 128), ceil(d_in / 128)]
+
+    def _c(self):
+        return _Fp8Weight(self.d_out, self.d_in, self.codes.data_ptr(), self.scales.data_ptr())
+
+    @staticmethod
+    def empty(d_out: int, d_in: int, device) -> "Fp8Weight":
+        return Fp8Weight(d_out, d_in, torch.empty(d_out, d_in, dtype=E4M3, device=device),
+                         torch.empty(_groups(d_out), _groups(d_in), dtype=torch.float32, device=device))
+
+
+def qlora_fp8_storage_bytes(d_out: int, d_in: int) -> int:
+    return int(_lib.qlora_fp8_storage_bytes(d_out, d_in))
+
+
+def qlora_fp8_workspace_bytes(d_out: int, d_in: int, T: int, r: int) -> int:
+    return int(_lib.qlora_fp8_workspace_bytes(d_out, d_in, T, r))
+
+
+def _check_fp8_weight(w: Fp8Weight):
+    if w.d_out < 16 or w.d_in < 16 or w.d_out % 16 or w.d_in % 16:
+        raise ValueError(f"weight shape {w.d_out}x{w.d_in}: both must be positive multiples of 16")
+    _arg(w.codes, "codes", E4M3, (w.d_out, w.d_in))
+    _arg(w.scales, "scales", torch.float32, (_groups(w.d_out), _groups(w.d_in)))
+
+
+def qlora_fp8_quantize(W: torch.Tensor, out: Fp8Weight | None = None) -> Fp8Weight:
+    """W (float32 or bfloat16 [d_out, d_in]) to e4m3 with scale amax / 448 per 128 x 128 block."""
+    dt = _float(W, "W")
+    if W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be a contiguous 2-D tensor")
+    d_out, d_in = W.shape
+    if out is None:
+        if d_out % 16 or d_in % 16:
+            raise ValueError(f"weight shape {d_out}x{d_in}: both must be positive multiples of 16")
+        out = Fp8Weight.empty(d_out, d_in, W.device)
+    if (out.d_out, out.d_in) != (d_out, d_in):
+        raise ValueError(f"out is {out.d_out}x{out.d_in}, W is {d_out}x{d_in}")
+    _check_fp8_weight(out)
+    _check_no_overlap({"W": W}, {"codes": out.codes, "scales": out.scales})
+    _check_devices(W.device, codes=out.codes, scales=out.scales)
+    cw = out._c()
+    with _on(W.device):
+        _check(_lib.qlora_fp8_quantize(_ptr(W), dt, ctypes.byref(cw), _stream(W.device)), "qlora_fp8_quantize")
+    return out
+
+
+def qlora_fp8_quantize_rows(x: torch.Tensor, fmt=E4M3, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None):
+    """Rows x [T, d] (float32 or bfloat16, d % 16 == 0) to 8 bits in groups of 128 with power-of-two scales.
+    Returns (xq fmt [T, d], xs float32 [T, ceil(d / 128)])."""
+    dt, f = _float(x, "x"), _fmt(fmt)
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D tensor")
+    T, d = x.shape
+    if T < 1 or d < 16 or d % 16:
+        raise ValueError(f"x must be [T >= 1, d] with d a positive multiple of 16, got {tuple(x.shape)}")
+    _arg(xq, "xq", fmt, (T, d))
+    _arg(xs, "xs", torch.float32, (T, _groups(d)))
+    _check_no_overlap({"x": x}, {"xq": xq, "xs": xs})
+    _check_devices(x.device, xq=xq, xs=xs)
+    if xq is None:
+        xq = torch.empty(T, d, dtype=fmt, device=x.device)
+    if xs is None:
+        xs = torch.empty(T, _groups(d), dtype=torch.float32, device=x.device)
+    with _on(x.device):
+        _check(_lib.qlora_fp8_quantize_rows(_ptr(x), dt, T, d, f, _ptr(xq), _ptr(xs), _stream(x.device)),
+               "qlora_fp8_quantize_rows")
+    return xq, xs
+
+
+def qlora_fp8_forward(w: Fp8Weight, x: torch.Tensor | None, A: torch.Tensor | None, B: torch.Tensor | None,
+                      alpha: float, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None, fmt=E4M3,
+                      save_u: bool = False, h: torch.Tensor | None = None, u: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None):
+    """h = xq W_hat^T (block-scaled) + (alpha/r) (x A^T) B^T over the 8-bit base. Returns (h bf16 [T, d_out], u).
+
+    xq, xs: the 8-bit rows of a norm or of qlora_fp8_quantize_rows, in fmt; without them x (bf16 [T, d_in]) is
+    quantized to fmt within the call. x itself is needed then, and for the adapter. u is float32 [T, r] when
+    save_u or given, else None."""
+    _check_fp8_weight(w)
+    f = _fmt(fmt)
+    if (xq is None) != (xs is None):
+        raise ValueError("give both xq and xs, or neither")
+    lead = x if x is not None else xq
+    if lead is None:
+        raise ValueError("give x, or xq and xs")
+    if not torch.is_tensor(lead) or lead.dim() != 2:
+        raise ValueError("x and xq must be 2-D [T, d_in] tensors")
+    T = lead.shape[0]
+    if T < 1:
+        raise ValueError("x must have at least one row")
+    _arg(x, "x", torch.bfloat16, (T, w.d_in))
+    _arg(xq, "xq", fmt, (T, w.d_in))
+    _arg(xs, "xs", torch.float32, (T, _groups(w.d_in)))
+    r = _adapter_rank(w, A, B)
+    if r and x is None:
+        raise ValueError("the adapter needs x")
+    _arg(h, "h", torch.bfloat16, (T, w.d_out))
+    if u is not None and r == 0:
+        raise ValueError("u is given but there is no adapter")
+    _arg(u, "u", torch.float32, (T, r))
+    nbytes = qlora_fp8_workspace_bytes(w.d_out, w.d_in, T, r)
+    if h is not None or u is not None or ws is not None:
+        _check_no_overlap({"x": x, "xq": xq, "xs": xs, "A": A, "B": B, "codes": w.codes, "scales": w.scales},
+                          {"h": h, "u": u, "ws": ws})
+    dev = w.codes.device
+    _check_devices(dev, scales=w.scales, x=x, xq=xq, xs=xs, A=A, B=B, h=h, u=u, ws=ws)
+    if h is None:
+        h = torch.empty(T, w.d_out, dtype=torch.bfloat16, device=dev)
+    if u is None and save_u and r > 0:
+        u = torch.empty(T, r, dtype=torch.float32, device=dev)
+    cw = w._c()
+    with _on(dev):
+        ws = _call_ws(dev, nbytes, ws)
+        _check(_lib.qlora_fp8_forward(ctypes.byref(cw), _ptr(xq), _ptr(xs), f, _ptr(x), T, _ptr(A), _ptr(B), r, alpha,
+                                      _ptr(h), _ptr(u), _ptr(ws), ws.numel(), _stream(dev)), "qlora_fp8_forward")
+    return h, u
+
+
+def qlora_fp8_backward(w: Fp8Weight, x: torch.Tensor | None, dY: torch.Tensor, A: torch.Tensor | None,
+                       B: torch.Tensor | None, alpha: float, u_saved: torch.Tensor | None = None, need_dx: bool = True,
+                       need_dA: bool = True, need_dB: bool = True, fmt=E4M3, dX: torch.Tensor | None = None,
+                       dA: torch.Tensor | None = None, dB: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """Returns (dX bf16 [T, d_in] | None, dA f32 [r, d_in] | None, dB f32 [d_out, r] | None); dY is quantized to fmt
+    within the call for dX's product with the base, and used as it is for the adapter."""
+    _check_fp8_weight(w)
+    f = _fmt(fmt)
+    if not torch.is_tensor(dY) or dY.dim() != 2 or dY.shape[0] < 1:
+        raise ValueError("dY must be a 2-D [T >= 1, d_out] tensor")
+    T = dY.shape[0]
+    _arg(dY, "dY", torch.bfloat16, (T, w.d_out))
+    _arg(x, "x", torch.bfloat16, (T, w.d_in))
+    r = _adapter_rank(w, A, B)
+    if r == 0 and (dA is not None or dB is not None or u_saved is not None):
+        raise ValueError("dA, dB and u_saved need an adapter")
+    _arg(u_saved, "u_saved", torch.float32, (T, r))
+    _arg(dX, "dX", torch.bfloat16, (T, w.d_in))
+    _arg(dA, "dA", torch.float32, (r, w.d_in))
+    _arg(dB, "dB", torch.float32, (w.d_out, r))
+    need_dA, need_dB = r > 0 and (need_dA or dA is not None), r > 0 and (need_dB or dB is not None)
+    if x is None and (need_dA or (need_dB and u_saved is None)):
+        raise ValueError("dA needs x, and dB needs x or u_saved")
+    nbytes = qlora_fp8_workspace_bytes(w.d_out, w.d_in, T, r)
+    if dX is not None or dA is not None or dB is not None or ws is not None:
+        _check_no_overlap({"x": x, "dY": dY, "A": A, "B": B, "u_saved": u_saved, "codes": w.codes, "scales": w.scales},
+                          {"dX": dX, "dA": dA, "dB": dB, "ws": ws})
+    dev = w.codes.device
+    _check_devices(dev, scales=w.scales, x=x, dY=dY, A=A, B=B, u_saved=u_saved, dX=dX, dA=dA, dB=dB, ws=ws)
+    if dX is None and need_dx:
+        dX = torch.empty(T, w.d_in, dtype=torch.bfloat16, device=dev)
+    if dA is None and need_dA:
+        dA = torch.empty(r, w.d_in, dtype=torch.float32, device=dev)
+    if dB is None and need_dB:
+        dB = torch.empty(w.d_out, r, dtype=torch.float32, device=dev)
+    cw = w._c()
+    with _on(dev):
+        ws = _call_ws(dev, nbytes, ws)
+        _check(_lib.qlora_fp8_backward(ctypes.byref(cw), _ptr(x), _ptr(dY), f, T, _ptr(A), _ptr(B), r, alpha,
+                                       _ptr(u_saved), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(dev)),
+               "qlora_fp8_backward")
+    return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# the root-mean-square norm
+# ---------------------------------------------------------------------------
+
+class RMSNormOut(NamedTuple):
+    y: torch.Tensor | None     # x's dtype [T, d]
+    yq: torch.Tensor | None    # fmt [T, d]
+    ys: torch.Tensor | None    # float32 [T, ceil(d / 128)]
+    s: torch.Tensor | None     # x + residual in x's dtype, when a residual was given
+    rstd: torch.Tensor | None  # float32 [T]
+
+
+def _rows(t, name: str, dtype, T: int, d: int):
+    """A [T, d] tensor of `dtype` whose rows are dense (any row stride of at least d)."""
+    if t is None:
+        return
+    if not torch.is_tensor(t):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != d:
+        raise ValueError(f"{name} must have shape {(T, d)}, got {tuple(t.shape)}")
+    if (d > 1 and t.stride(1) != 1) or (T > 1 and t.stride(0) < d):
+        raise ValueError(f"{name} must have dense rows that do not overlap, got strides {t.stride()}")
+
+
+def _row_stride(t, d: int) -> int:
+    return d if t is None or t.shape[0] <= 1 else t.stride(0)
+
+
+def _norm_weight(weight, d: int) -> int:
+    if weight is None:
+        return F32
+    wd = _float(weight, "weight")
+    _arg(weight, "weight", weight.dtype, (d,))
+    return wd
+
+
+def qlora_rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                          eps: float = 1e-6, want_y: bool = True, fmt=None, save_rstd: bool = False) -> RMSNormOut:
+    """s = x + residual (rounded to x's dtype); y = s / sqrt(mean(s^2) + eps) * weight over the rows of x [T, d]
+    (float32 or bfloat16, any row stride). y comes in x's dtype (want_y) and / or as 8-bit rows with scales (fmt:
+    torch.float8_e4m3fn or torch.float8_e5m2), as qlora_fp8_forward takes them."""
+    dt = _float(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a 2-D [T, d] tensor")
+    T, d = x.shape
+    if not 1 <= d <= NORM_MAX_DIM:
+        raise ValueError(f"rows of {d} values: 1 to {NORM_MAX_DIM}")
+    _rows(x, "x", x.dtype, T, d)
+    _rows(residual, "residual", x.dtype, T, d)
+    wd = _norm_weight(weight, d)
+    f = 0 if fmt is None else _fmt(fmt)
+    if not want_y and fmt is None:
+        raise ValueError("nothing to write: want_y is false and fmt is None")
+    dev = x.device
+    _check_devices(dev, weight=weight, residual=residual)
+    y = torch.empty(T, d, dtype=x.dtype, device=dev) if want_y else None
+    s = torch.empty(T, d, dtype=x.dtype, device=dev) if residual is not None else None
+    yq = ys = None
+    if fmt is not None:
+        yq = torch.empty(T, d, dtype=fmt, device=dev)
+        ys = torch.empty(T, _groups(d), dtype=torch.float32, device=dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if save_rstd else None
+    with _on(dev):
+        _check(_lib.qlora_rmsnorm_forward(_ptr(x), _row_stride(x, d), _ptr(residual), _row_stride(residual, d), dt, T, d,
+                                          _ptr(weight), wd, eps, _ptr(s), _ptr(y), _ptr(yq), _ptr(ys), f, _ptr(rstd),
+                                          _stream(dev)), "qlora_rmsnorm_forward")
+    return RMSNormOut(y, yq, ys, s, rstd)
+
+
+def qlora_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor | None, rstd: torch.Tensor,
+                           ds: torch.Tensor | None = None, need_dw: bool = False, ws: torch.Tensor | None = None):
+    """Returns (dx, dw): dx in s's dtype is the gradient of x and of the residual; dw float32 [d] when need_dw. dy is
+    the gradient of y, ds the one that reaches s past the norm (both in s's dtype, any row stride)."""
+    dt = _float(s, "s")
+    if s.dim() != 2:
+        raise ValueError("s must be a 2-D [T, d] tensor")
+    T, d = s.shape
+    if not 1 <= d <= NORM_MAX_DIM:
+        raise ValueError(f"rows of {d} values: 1 to {NORM_MAX_DIM}")
+    _rows(s, "s", s.dtype, T, d)
+    if dy is None:
+        raise TypeError("dy must be a tensor")
+    _rows(dy, "dy", s.dtype, T, d)
+    _rows(ds, "ds", s.dtype, T, d)
+    wd = _norm_weight(weight, d)
+    if rstd is None:
+        raise TypeError("rstd must be a tensor")
+    _arg(rstd, "rstd", torch.float32, (T,))
+    dev = s.device
+    _check_devices(dev, dy=dy, ds=ds, weight=weight, rstd=rstd, ws=ws)
+    dx = torch.empty(T, d, dtype=s.dtype, device=dev)
+    dw = torch.empty(d, dtype=torch.float32, device=dev) if need_dw else None
+    with _on(dev):
+        nbytes = 0
+        if need_dw:  # the partial sums of dw: scratch of this call alone
+            nbytes = int(_lib.qlora_rmsnorm_workspace_bytes(T, d))
+            if ws is not None:
+                _check_no_overlap({"dy": dy, "s": s, "ds": ds, "weight": weight, "rstd": rstd},
+                                  {"ws": _own_workspace(ws, nbytes)})
+            else:
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(_lib.qlora_rmsnorm_backward(_ptr(dy), _row_stride(dy, d), _ptr(s), _row_stride(s, d), _ptr(ds),
+                                           _row_stride(ds, d), dt, T, d, _ptr(weight), wd, _ptr(rstd), _ptr(dx), _ptr(dw),
+                                           _ptr(ws) if need_dw else None, nbytes, _stream(dev)),
+               "qlora_rmsnorm_backward")
+    return dx, dw
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------
+
+def adamw_state_elements(sizes) -> int:
+    """Elements of the flat state of tensors of these sizes: each starts at a multiple of 256."""
+    return sum(-(-n // ADAMW_BLOCK) * ADAMW_BLOCK for n in sizes)
+
+
+def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor, m_scale: torch.Tensor | None = None,
+                     v_scale: torch.Tensor | None = None, master: torch.Tensor | None = None, lr: float = 1e-4,
+                     beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
+                     max_norm: float | None = None, seed: int = 0, norm: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None) -> torch.Tensor | None:
+    """One AdamW step over lists of gradients (all float32 or all bfloat16) and parameters (all float32, or all
+    bfloat16 with a float32 `master` copy), in place.
+
+    m, v, master are flat: tensor i's elements start after those of the tensors before it, each rounded up to a
+    multiple of 256 (adamw_state_elements of the sizes in all). float32 m and v hold the moments; float8_e4m3fn ones
+    hold 8-bit codes of m and sqrt(v), with float32 m_scale and v_scale per 256 elements, rounded stochastically by
+    bits that depend on (seed, step, place) alone. max_norm: gradients are scaled to at most that global norm first,
+    and a norm that is not finite leaves everything as it was; the norm is returned (float32 [1], on the device)."""
+    grads, params = list(grads), list(params)
+    count = len(grads)
+    if len(params) != count:
+        raise ValueError(f"{count} gradients but {len(params)} parameters")
+    if not torch.is_tensor(m) or not torch.is_tensor(v):
+        raise TypeError("m and v must be tensors")
+    dev = m.device
+    gd, pd = (grads[0].dtype, params[0].dtype) if count else (torch.float32, torch.float32)
+    if gd not in _FLOAT or pd not in _FLOAT:
+        raise TypeError(f"gradients and parameters must be float32 or bfloat16, got {gd} and {pd}")
+    jobs = (_AdamWJob * max(count, 1))()
+    total, spans = 0, []
+    for i in range(count):
+        g, p = grads[i], params[i]
+        n = p.numel()
+        if g.dtype is not gd or p.dtype is not pd:
+            raise TypeError(f"tensor {i}: all gradients must be {gd} and all parameters {pd}")
+        if g.numel() != n or not g.is_contiguous() or not p.is_contiguous():
+            raise ValueError(f"tensor {i}: gradient and parameter must be contiguous and of one size")
+        if g.device != dev or p.device != dev:
+            raise ValueError(f"tensor {i} is on {g.device} / {p.device}, the state on {dev}")
+        j = jobs[i]
+        at = p.data_ptr()
+        j.grad, j.param, j.n = g.data_ptr(), at, n
+        total += -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
+        if n:
+            spans.append((at, at + n * p.element_size()))
+    spans.sort()
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("parameters overlap (is one listed twice?)")
+    bits8 = m.dtype == E4M3
+    if not bits8 and m.dtype != torch.float32:
+        raise TypeError(f"m must be float32 or float8_e4m3fn, got {m.dtype}")
+    _arg(m, "m", m.dtype, (total,))
+    _arg(v, "v", m.dtype, (total,))
+    if bits8 != (m_scale is not None) or bits8 != (v_scale is not None):
+        raise ValueError("8-bit moments need m_scale and v_scale, 32-bit ones take none")
+    _arg(m_scale, "m_scale", torch.float32, (total // ADAMW_BLOCK,))
+    _arg(v_scale, "v_scale", torch.float32, (total // ADAMW_BLOCK,))
+    if count and (pd == torch.bfloat16) != (master is not None):
+        raise ValueError("bfloat16 parameters need a float32 master copy, float32 ones take none")
+    _arg(master, "master", torch.float32, (total,))
+    if not 0 <= int(seed) < 1 << 32:
+        raise ValueError("seed must fit in 32 bits")
+    _arg(norm, "norm", torch.float32, (1,))
+    if max_norm is None and norm is not None:
+        raise ValueError("norm is given but max_norm is not")
+    if max_norm is not None and not max_norm > 0:
+        raise ValueError(f"max_norm must be positive, got {max_norm}")
+    _check_devices(dev, v=v, m_scale=m_scale, v_scale=v_scale, master=master, norm=norm, ws=ws)
+    hp = _AdamWManyHparams(lr, beta1, beta2, eps, weight_decay)
+    st = _AdamWState(2 if bits8 else 0, m.data_ptr(), v.data_ptr(), _ptr(m_scale), _ptr(v_scale), _ptr(master))
+    with _on(dev):
+        nbytes = 0
+        if max_norm is not None:
+            if norm is None:
+                norm = torch.empty(1, dtype=torch.float32, device=dev)
+            nbytes = int(_lib.qlora_adamw_many_workspace_bytes(count))
+            # partial sums, scratch of this call alone
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if ws is None else _own_workspace(ws, nbytes)
+        _check(_lib.qlora_adamw_many(ctypes.byref(hp), step, jobs, count, _FLOAT[gd], _FLOAT[pd], ctypes.byref(st),
+                                     0.0 if max_norm is None else max_norm, _ptr(norm), int(seed),
+                                     None if max_norm is None else _ptr(ws), nbytes, _stream(dev)), "qlora_adamw_many")
+    return norm

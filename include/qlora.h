@@ -54,6 +54,9 @@ extern "C" {
 #define QLORA_MAX_TOKENS (1 << 24)       /* T upper bound                      */
 #define QLORA_WS_COUNTER_BYTES 65536     /* zeroed counter region of a workspace */
 #define QLORA_STATIC_SCRATCH_BYTES (1u << 20) /* scratch of qlora_forward_noalloc per GPU */
+#define QLORA_FP8_GROUP 128         /* values of a row, rows and columns of a weight block, per 8-bit scale */
+#define QLORA_NORM_MAX_DIM 32768    /* widest row of the root-mean-square norm */
+#define QLORA_ADAMW_BLOCK 256       /* elements of a moment per scale; tensors start at multiples of it */
 
 typedef enum {
   QLORA_OK = 0,
@@ -72,7 +75,8 @@ typedef enum {
                                than QLORA_STATIC_SCRATCH_BYTES                 */
 } qlora_status;
 
-typedef enum { QLORA_F32 = 0, QLORA_BF16 = 1 } qlora_dtype;
+/* E4M3 and E5M2 are the 8-bit formats of torch's float8_e4m3fn and float8_e5m2. */
+typedef enum { QLORA_F32 = 0, QLORA_BF16 = 1, QLORA_E4M3 = 2, QLORA_E5M2 = 3 } qlora_dtype;
 
 /*
  * A quantized frozen weight W [d_out, d_in] (d_in % 64 == 0), n = d_out*d_in,
@@ -281,6 +285,163 @@ int qlora_adamw_step(const qlora_adamw_hparams *hp, int64_t step, int64_t n, con
  */
 int qlora_adamw_step_host(const qlora_adamw_hparams *hp, int64_t step, int64_t n, const float *grad, float *master,
                           float *m, float *v, uint16_t *param, int32_t threads);
+
+/*
+ * The frozen base in 8-bit floating point, beside the 4-bit storage: e4m3 codes
+ * and one float32 scale per block of 128 x 128 weights (the last blocks of a
+ * row or column may be cut),
+ *   codes  [d_out, d_in]                              u8 (e4m3 bit patterns), row-major
+ *   scales [ceil(d_out / 128), ceil(d_in / 128)]      f32
+ * W_hat[n, k] = codes[n, k] * scales[n / 128, k / 128]. Any finite scales are
+ * taken (a checkpoint's own, or qlora_fp8_quantize's). d_out % 16 == 0,
+ * d_in % 16 == 0, both <= QLORA_MAX_DIM.
+ *
+ * Rows (activations, upstream gradients) are 8-bit values with one float32 scale
+ * per 128 consecutive values: codes [T, d], scales [T, ceil(d / 128)].
+ */
+typedef struct {
+  int64_t d_out;
+  int64_t d_in;
+  uint8_t *codes;
+  float *scales;
+} qlora_fp8_weight;
+
+/* Bytes of an 8-bit weight: n + 4 * ceil(d_out / 128) * ceil(d_in / 128). */
+size_t qlora_fp8_storage_bytes(int64_t d_out, int64_t d_in);
+
+/*
+ * Quantize a weight [d_out, d_in] (f32 or bf16) once: per block, scale =
+ * amax / 448 and codes = e4m3(w * (448 / amax)), nearest, ties to even (amax is
+ * taken as at least 2^-100). A block that holds a NaN or an infinity restores to
+ * values that are not finite. Errors: NULL, SHAPE, DTYPE, ALIGN, HIP.
+ */
+int qlora_fp8_quantize(const void *W, int w_dtype, const qlora_fp8_weight *out, hipStream_t stream);
+
+/*
+ * Quantize rows x [T, d] (f32 or bf16; d % 16 == 0) to fmt (QLORA_E4M3 or
+ * QLORA_E5M2): per group of 128, scale = the least power of two with amax <=
+ * MAX * scale (MAX = 448 or 57344; amax at least 2^-100), codes = x / scale
+ * (exact), nearest, ties to even. A group that holds a NaN or an infinity gives
+ * products that are not finite. Errors: NULL, DTYPE, SHAPE, ALIGN, HIP.
+ */
+int qlora_fp8_quantize_rows(const void *x, int x_dtype, int64_t T, int64_t d, int fmt, uint8_t *codes, float *scales,
+                            hipStream_t stream);
+
+/* Workspace bytes sufficient for both qlora_fp8_forward and qlora_fp8_backward at these sizes. */
+size_t qlora_fp8_workspace_bytes(int64_t d_out, int64_t d_in, int64_t T, int32_t r);
+
+/*
+ * Forward over the 8-bit base,
+ *   h = sum over blocks b of 128: xs[t, b] scales[n / 128, b] (xq_b . codes_b)  +  (alpha/r) (x A^T) B^T,
+ * block products and their sum in float32, one rounding to bf16.
+ *   xq, xs  the 8-bit rows (fmt) and their scales [T, ceil(d_in / 128)]; both
+ *           NULL: x is quantized within the call (qlora_fp8_quantize_rows' rule)
+ *   x       bf16 [T, d_in]; may be NULL with xq given and no adapter
+ *   A, B, r, alpha, h, u_out, ws: as for qlora_forward; ws at least
+ *           qlora_fp8_workspace_bytes(d_out, d_in, T, r) bytes with its counters
+ *           zero, which every call leaves zero (a workspace may serve
+ *           qlora_forward and this call in turn)
+ * Errors: NULL, DTYPE, SHAPE, ALIGN, WORKSPACE, HIP.
+ */
+int qlora_fp8_forward(const qlora_fp8_weight *W, const uint8_t *xq, const float *xs, int fmt, const uint16_t *x,
+                      int64_t T, const uint16_t *A, const uint16_t *B, int32_t r, float alpha, uint16_t *h,
+                      float *u_out, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Backward through the frozen 8-bit base: dX = dYq W_hat + (alpha/r) v A with dY
+ * quantized within the call to fmt along d_out (the adapter terms use dY
+ * itself), v, dA and dB as in qlora_backward. No gradient flows into W.
+ * Arguments as for qlora_backward. Errors: as qlora_fp8_forward.
+ */
+int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint16_t *dY, int fmt, int64_t T,
+                       const uint16_t *A, const uint16_t *B, int32_t r, float alpha, const float *u_saved, uint16_t *dX,
+                       float *dA, float *dB, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of rows [T, d], with the residual's addition before it:
+ *   s = x + residual (rounded to dtype; s = x without one),
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight
+ * in float32. y is written in dtype, and / or as 8-bit rows (fmt) with scales by
+ * qlora_fp8_quantize_rows' rule from the float32 y.
+ *   x, residual  dtype (f32 or bf16) [T, d], rows ldx and ldr elements apart
+ *                (>= d), aligned to their element; residual NULL: none
+ *   weight       w_dtype (f32 or bf16) [d], NULL: ones
+ *   s            dtype [T, d], given exactly when residual is
+ *   y            dtype [T, d], nullable;  yq [T, d] with ys [T, ceil(d / 128)],
+ *                both nullable, one of y and yq wanted
+ *   rstd         f32 [T], nullable
+ * 0 <= T, 1 <= d <= QLORA_NORM_MAX_DIM, any d. Outputs are dense, 16-byte
+ * aligned, and may not overlap an input. Errors: DTYPE, SHAPE, VALUE (eps not a finite number >= 0), NULL,
+ * ALIGN, HIP.
+ */
+int qlora_rmsnorm_forward(const void *x, int64_t ldx, const void *residual, int64_t ldr, int dtype, int64_t T, int64_t d,
+                          const void *weight, int w_dtype, float eps, void *s, void *y, uint8_t *yq, float *ys, int fmt,
+                          float *rstd, hipStream_t stream);
+
+/*
+ * Its backward, from dy (the gradient of y; of yq's values where those were
+ * used) and ds (the gradient that reaches s past the norm, nullable):
+ *   g = dy * weight, xh = s * rstd:  dx = ds + rstd (g - xh mean(g xh)),
+ *   dw = sum over rows of dy * xh
+ * dx (dtype [T, d]) is the gradient of x and of the residual alike. dw f32 [d],
+ * nullable; it needs ws of qlora_rmsnorm_workspace_bytes(T, d) bytes (no
+ * initialisation). T = 0 writes zeros to dw. Errors: as the forward's, WORKSPACE.
+ */
+int qlora_rmsnorm_backward(const void *dy, int64_t ldy, const void *s, int64_t lds, const void *ds, int64_t ldd,
+                           int dtype, int64_t T, int64_t d, const void *weight, int w_dtype, const float *rstd, void *dx,
+                           float *dw, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlora_rmsnorm_workspace_bytes(int64_t T, int64_t d);
+
+/*
+ * One AdamW step over `count` tensors in a few launches (128 tensors each), the
+ * arithmetic of qlora_adamw_step, with the gradients scaled to a global norm and
+ * the moments in 32 bits or in 8.
+ *   jobs     host array: each tensor's gradient (grad_dtype f32 or bf16),
+ *            parameter (param_dtype f32: updated in place; bf16: receives
+ *            bf16(master)) and number of elements (0 is allowed)
+ *   state    host struct; tensor i's elements begin at off_i = the sum over the
+ *            tensors before it of n rounded up to QLORA_ADAMW_BLOCK:
+ *              dtype QLORA_F32   m, v f32
+ *              dtype QLORA_E4M3  m and v e4m3 codes of m and of sqrt(v), with
+ *                                m_scale, v_scale f32 per block of 256: the
+ *                                values are code * scale (the root's, squared, is v)
+ *              master            f32 copy of the parameters, for bf16 ones
+ *            elements between a tensor's end and the next block are not touched
+ *   max_norm > 0: gradients are multiplied by min(1, max_norm / (norm + 1e-6)),
+ *            norm the 2-norm over all of them (summed in float64), written to
+ *            *norm (device f32). When it is not finite, every parameter and
+ *            moment stays as it was. 0: no clipping, norm and ws may be NULL
+ *   seed     8-bit moments are rounded stochastically, by bits that depend on
+ *            (seed, step, the element's place): the same call gives the same bits
+ *   ws       qlora_adamw_many_workspace_bytes(count) bytes (no initialisation)
+ * All device memory, 16-byte aligned. n < 2^38, fewer than 2^31 blocks in all.
+ * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, HIP.
+ */
+typedef struct {
+  const void *grad;
+  void *param;
+  int64_t n;
+} qlora_adamw_job;
+typedef struct {
+  int dtype;
+  void *m;
+  void *v;
+  float *m_scale;
+  float *v_scale;
+  float *master;
+} qlora_adamw_state;
+/* As qlora_adamw_hparams, in float64: 1 - beta2 of a float32 beta2 = 0.999 is off by 1.3e-5 of itself. */
+typedef struct {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+} qlora_adamw_many_hparams;
+int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlora_adamw_job *jobs, int32_t count,
+                     int grad_dtype, int param_dtype, const qlora_adamw_state *state, float max_norm, float *norm,
+                     uint32_t seed, void *ws, size_t ws_bytes, hipStream_t stream);
+size_t qlora_adamw_many_workspace_bytes(int32_t count);
 
 /*
  * For callers that cannot allocate (code under HIP graph capture, tight

@@ -1,0 +1,320 @@
+"""The 8-bit frozen base on the GPU (needs an MI355X): the quantizers bit for bit, the forward and backward against
+64-bit references within bounds counted from the formats, cut blocks, single tokens, any finite scales, values that
+are not finite, rows past the last token, streams, and calls captured into a graph."""
+
+import zlib
+
+import pytest
+import torch
+
+import ops_ref as R
+from gpu_common import product, say
+
+pytestmark = pytest.mark.gpu
+
+q = product("qlora")
+FMTS = [R.E4M3, R.E5M2]
+
+
+def _gen(*key):
+    return torch.Generator(device="cuda").manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _rows(g, T, d):
+    x = _randn(g, T, d) * torch.exp2(torch.randint(-6, 7, (T, 1), generator=g, device="cuda").float())
+    return (x * (1 + 15 * (torch.rand(d, generator=g, device="cuda") < 0.02))).bfloat16()
+
+
+def _weight(g, N, K, scales="amax"):
+    w = q.qlora_fp8_quantize(_randn(g, N, K) * 0.02)
+    if scales == "any":  # a checkpoint's own: of any size and sign, some zero
+        s = _randn(g, *w.scales.shape) * 1e-3
+        s[torch.rand(s.shape, generator=g, device="cuda") < 0.1] = 0
+        w.scales.copy_(s)
+    return w
+
+
+def _adapter(g, N, K, r):
+    if not r:
+        return None, None
+    return (_randn(g, r, K) * 0.02).bfloat16(), (_randn(g, N, r) * 0.02).bfloat16()
+
+
+def _check(name, got, ref, bound):
+    got = got.double()
+    assert got.shape == ref.shape and torch.isfinite(got).all(), name
+    worst = ((got - ref).abs() / bound.clamp_min(1e-300)).max().item()
+    say(f"    {name}: largest error / bound = {worst:.3f}")
+    assert worst <= 1.0, f"{name}: {worst} times the bound"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,d", [(1, 16), (1, 128), (3, 144), (7, 2048), (5, 2064), (33, 5120)])
+def test_quantize_rows_bit_exact(T, d, dtype, fmt):
+    say(f"fp8 rows {T}x{d} {dtype} {fmt}")
+    g = _gen(T, d)
+    x = _rows(g, T, d).to(dtype)
+    if dtype is torch.float32:
+        x = x + _randn(g, T, d) * 1e-3
+    x[0, : min(d, 128)] = 0  # a group of zeros
+    xq, xs = q.qlora_fp8_quantize_rows(x, fmt)
+    codes, scales = R.quantize_rows(x, fmt)
+    assert torch.equal(xs.double(), scales)
+    assert torch.equal(xq.double(), codes)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_rows_extremes(fmt):
+    """The largest values of a binade on both sides of 1.75, subnormal bf16, the largest finite value."""
+    say(f"fp8 rows extremes {fmt}")
+    x = torch.zeros(6, 128, device="cuda")
+    x[0, 0], x[1, 0], x[2, 0] = 1.75, 1.75 + 2.0 ** -22, 1.9999
+    x[3, 0], x[3, 1] = 2.0 ** -133, -(2.0 ** -130)
+    x[4, 0], x[4, 1] = 3.3895313892515355e38, -1e30
+    x[5] = torch.linspace(-448, 448, 128, device="cuda")
+    xq, xs = q.qlora_fp8_quantize_rows(x, fmt)
+    codes, scales = R.quantize_rows(x, fmt)
+    assert torch.equal(xs.double(), scales) and torch.equal(xq.double(), codes)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(16, 16), (128, 128), (144, 272), (400, 1040)])
+def test_quantize_weight(N, K, dtype):
+    """scale = amax / 448 to one float32 rounding; every code is the nearest value of w * (448 / amax), up to the two
+    float32 roundings of that product (a code may fall on the other side of a tie only when the exact quotient is
+    within 2^-22 of it)."""
+    say(f"fp8 weight {N}x{K} {dtype}")
+    W = (_randn(_gen(N, K), N, K) * 0.02).to(dtype)
+    w = q.qlora_fp8_quantize(W)
+    amax = R.block_amax(W)
+    assert ((w.scales.double() - amax / 448).abs() <= 2.0 ** -24 * amax / 448).all()
+    x = W.double() * (448 / amax).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    step = torch.exp2((torch.frexp(x)[1] - 1).clamp_min(-6).double() - 3)
+    assert ((w.codes.double() - x).abs() <= step / 2 + 2.0 ** -22 * x.abs()).all()
+
+
+SHAPES = [  # T, d_out, d_in, r
+    (1, 16, 16, 0), (1, 128, 128, 8), (1, 1040, 2064, 16), (2, 400, 144, 24), (15, 256, 512, 0), (16, 1024, 1024, 64),
+    (17, 272, 400, 8), (33, 528, 1296, 16), (64, 256, 256, 256), (65, 128, 4096, 8), (100, 640, 784, 40),
+    (255, 256, 384, 0), (256, 512, 512, 16), (257, 784, 656, 64), (515, 1808, 1040, 8), (1030, 272, 2576, 0),
+]
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("T,N,K,r", SHAPES)
+def test_forward(T, N, K, r, given):
+    fmt = FMTS[(T + N // 16) % 2]
+    say(f"fp8 forward T={T} {N}x{K} r={r} {fmt} given={given}")
+    g = _gen(T, N, K, r, given)
+    w = _weight(g, N, K, "any" if given else "amax")
+    x = _rows(g, T, K)
+    A, B = _adapter(g, N, K, r)
+    xq, xs = q.qlora_fp8_quantize_rows(x, fmt)
+    if given:  # scales of any kind
+        xs = xs * (0.5 + torch.rand(xs.shape, generator=g, device="cuda"))
+    big = torch.full((T + 3, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    h, u = q.qlora_fp8_forward(w, x, A, B, 16.0, xq=xq if given else None, xs=xs if given else None, fmt=fmt,
+                               save_u=True, h=big[:T])
+    assert h.data_ptr() == big.data_ptr() and (big[T:] == 7).all()
+    xh, wh = xq.double() * R.spread_cols(xs, K), R.restored_weight(w.codes, w.scales)
+    ref, extra = xh @ wh.t(), 0.0
+    if r:
+        s = 16.0 / r
+        uref = x.double() @ A.double().t()
+        umag = x.double().abs() @ A.double().abs().t()
+        # u: float32 sums of exact products; s u is rounded to bf16 (half a step) before its product with B
+        ubound = (K + 4) * 2.0 ** -23 * umag
+        _check("u", u, uref, ubound)
+        ref = ref + s * uref @ B.double().t()
+        extra = s * ((2.0 ** -8 * uref.abs() + (1 + 2.0 ** -8) * ubound) @ B.double().abs().t()
+                     + (r + 4) * 2.0 ** -23 * uref.abs() @ B.double().abs().t())
+    else:
+        assert u is None
+    _check("h", h, ref, R.product_bound(xh, wh, ref, extra))
+    h2, _ = q.qlora_fp8_forward(w, x, A, B, 16.0, xq=xq if given else None, xs=xs if given else None, fmt=fmt)
+    assert torch.equal(h2, h)
+
+
+@pytest.mark.parametrize("T,N,K,r", SHAPES)
+def test_backward(T, N, K, r):
+    fmt = FMTS[(T + K // 16) % 2]
+    say(f"fp8 backward T={T} {N}x{K} r={r} {fmt}")
+    g = _gen(T, N, K, r, "b")
+    w = _weight(g, N, K, "any")
+    x, dY = _rows(g, T, K), _rows(g, T, N)
+    A, B = _adapter(g, N, K, r)
+    big = torch.full((T + 2, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    dX, dA, dB = q.qlora_fp8_backward(w, x, dY, A, B, 16.0, fmt=fmt, dX=big[:T])
+    assert (big[T:] == 7).all()
+    codes, scales = R.quantize_rows(dY, fmt)
+    yh, wh = codes * R.spread_cols(scales, N), R.restored_weight(w.codes, w.scales).t()
+    ref, extra = yh @ wh.t(), 0.0
+    if r:
+        s, D, Bd, Ad, X = 16.0 / r, dY.double(), B.double(), A.double(), x.double()
+        v, vb = D @ Bd, (N + 4) * 2.0 ** -23 * (D.abs() @ Bd.abs())
+        ref = ref + s * v @ Ad
+        extra = s * ((2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * vb) @ Ad.abs() + (r + 4) * 2.0 ** -23 * v.abs() @ Ad.abs())
+        # dA, dB: a float32 operand enters the matrix units as two bf16 terms (what is left is below 2^-16 of it),
+        # float32 sums over the tokens
+        lim = 2.0 ** -16 + (T + 8) * 2.0 ** -23
+        _check("dA", dA, s * v.t() @ X, s * (lim * v.abs().t() + vb.t()) @ X.abs())
+        U, ub = X @ Ad.t(), (K + 4) * 2.0 ** -23 * (X.abs() @ Ad.abs().t())
+        _check("dB", dB, s * D.t() @ U, s * D.abs().t() @ (lim * U.abs() + ub))
+    else:
+        assert dA is None and dB is None
+    _check("dX", dX, ref, R.product_bound(yh, wh, ref, extra))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_what_the_matrix_unit_keeps(fmt):
+    """A large product and its negative beside a small one: among the same eight k the small one survives down to
+    2^-13 of the large one, in another eight down to 2^-23 at least. Every bound on a product here rests on it."""
+    say(f"fp8 matrix unit {fmt}")
+    for place in range(128):
+        if place in (3, 5):
+            continue
+        n = 13 if place < 8 else 23
+        small = 16 - n
+        x, w = torch.zeros(16, 128, device="cuda"), torch.zeros(16, 128, device="cuda")
+        x[:, 3], w[:, 3], x[:, 5], w[:, 5] = 256, 256, 256, -256
+        x[:, place], w[:, place] = 2.0 ** (small // 2), 2.0 ** (small - small // 2)
+        h, _ = q.qlora_fp8_forward(q.Fp8Weight(16, 128, w.to(R.E4M3), torch.ones(1, 1, device="cuda")), None, None, None,
+                                   1.0, xq=x.to(fmt), xs=torch.ones(16, 1, device="cuda"), fmt=fmt)
+        assert (h == 2.0 ** small).all(), place
+
+
+def test_adapter_gradients_against_differences():
+    """The loss sum(c * h) is bilinear in A and B: central differences of it in 64 bits are exact but for rounding."""
+    say("fp8 gradients against differences")
+    T, N, K, r = 20, 48, 80, 8
+    g = _gen("diff")
+    w = _weight(g, N, K)
+    x, c = _rows(g, T, K), _randn(g, T, N).bfloat16()
+    A, B = _adapter(g, N, K, r)
+    dX, dA, dB = q.qlora_fp8_backward(w, x, c, A, B, 16.0)
+    xd, cd, wh = x.double(), c.double(), R.restored_weight(w.codes, w.scales)
+
+    def loss(A, B, x=xd):
+        return (cd * (x @ wh.t() + 16.0 / r * (x @ A.t()) @ B.t())).sum()
+
+    Ad, Bd = A.double(), B.double()
+    for k in range(12):
+        dirA, dirB = torch.randn_like(Ad), torch.randn_like(Bd)
+        da = (loss(Ad + dirA, Bd) - loss(Ad - dirA, Bd)) / 2
+        db = (loss(Ad, Bd + dirB) - loss(Ad, Bd - dirB)) / 2
+        mag_a = ((cd.abs() @ Bd.abs()).t() @ xd.abs() * 2 * dirA.abs()).sum()
+        mag_b = (cd.abs().t() @ (xd.abs() @ Ad.abs().t()) * 2 * dirB.abs()).sum()
+        assert abs(da - (dA.double() * dirA).sum()) <= 2.0 ** -15 * mag_a
+        assert abs(db - (dB.double() * dirB).sum()) <= 2.0 ** -15 * mag_b
+        # in x: the base sees the gradient in 8 bits (half a step, 2^-4), the result is rounded to bf16 (2^-8)
+        dirx = torch.randn_like(xd)
+        dx = (loss(Ad, Bd, xd + dirx) - loss(Ad, Bd, xd - dirx)) / 2
+        lim = (2.0 ** -4 + 2.0 ** -10) * (cd.abs() @ wh.abs() * dirx.abs()).sum()
+        lim = lim + 2.0 ** -7 * (((cd.abs() @ Bd.abs()) @ Ad.abs() * 2 + cd.abs() @ wh.abs()) * dirx.abs()).sum()
+        assert abs(dx - (dX.double() * dirx).sum()) <= lim
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 300])
+def test_values_that_are_not_finite_stay_in_their_rows(T):
+    say(f"fp8 not finite T={T}")
+    N, K = 272, 400
+    g = _gen("nan", T)
+    w = _weight(g, N, K)
+    x = _rows(g, T, K)
+    clean, _ = q.qlora_fp8_forward(w, x, None, None, 1.0)
+    bad = x.clone()
+    bad[T // 2, 5] = float("nan")
+    bad[T - 1, 300] = float("inf")
+    h, _ = q.qlora_fp8_forward(w, bad, None, None, 1.0)
+    rows = sorted({T // 2, T - 1})
+    assert not torch.isfinite(h[rows]).any()
+    keep = [t for t in range(T) if t not in rows]
+    assert torch.equal(h[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_codes_of_nan_past_a_cut_block_are_not_read(T):
+    """d_in = 144: the second block holds 16 columns; what follows a row in memory (the next row's codes, here NaN
+    rows) does not reach it."""
+    say(f"fp8 cut block T={T}")
+    N, K = 64, 144
+    g = _gen("cut", T)
+    w = _weight(g, N, K)
+    x = _rows(g, T, K)
+    clean, _ = q.qlora_fp8_forward(w, x, None, None, 1.0)
+    codes = w.codes.view(torch.uint8).clone()
+    codes[1::2] = 0x7F
+    h, _ = q.qlora_fp8_forward(q.Fp8Weight(N, K, codes.view(R.E4M3), w.scales), x, None, None, 1.0)
+    assert torch.equal(h[:, 0::2], clean[:, 0::2]) and torch.isnan(h[:, 1::2]).all()
+
+
+def test_frozen_a_and_recomputed_u():
+    say("fp8 frozen A, recomputed u")
+    T, N, K, r = 70, 256, 512, 16
+    g = _gen("fa")
+    w, x, dY = _weight(g, N, K), _rows(g, T, K), _rows(g, T, N)
+    A, B = _adapter(g, N, K, r)
+    _, u = q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True)
+    full = q.qlora_fp8_backward(w, x, dY, A, B, 16.0)
+    dX, dA, dB = q.qlora_fp8_backward(w, None, dY, A, B, 16.0, u_saved=u, need_dA=False)
+    assert dA is None and torch.equal(dX, full[0]) and torch.equal(dB, full[2])
+
+
+def test_own_workspaces_on_two_streams():
+    say("fp8 two streams")
+    g = _gen("streams")
+    jobs = []
+    for T, N, K in ((16, 1024, 2048), (300, 528, 784)):
+        w, x = _weight(g, N, K), _rows(g, T, K)
+        A, B = _adapter(g, N, K, 16)
+        ws = torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, 16), dtype=torch.uint8, device="cuda")
+        jobs.append((w, x, A, B, ws, q.qlora_fp8_forward(w, x, A, B, 16.0)[0]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    outs = []
+    for _ in range(3):
+        for st, (w, x, A, B, ws, _) in zip(streams, jobs):
+            with torch.cuda.stream(st):
+                outs.append(q.qlora_fp8_forward(w, x, A, B, 16.0, ws=ws)[0])
+    torch.cuda.synchronize()
+    for i, h in enumerate(outs):
+        assert torch.equal(h, jobs[i % 2][5])
+
+
+@pytest.mark.parametrize("T", [1, 16, 100])
+def test_captured_calls(T):
+    """Forward and backward captured into two graphs, replayed in turn with eager calls between: every replay gives
+    the eager results for the inputs of the moment."""
+    say(f"fp8 graph T={T}")
+    N, K, r = 528, 1040, 16
+    g = _gen("graph", T)
+    w = _weight(g, N, K)
+    A, B = _adapter(g, N, K, r)
+    x, dY = _rows(g, T, K), _rows(g, T, N)
+    call = lambda: q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True)  # noqa: E731
+    back = lambda: q.qlora_fp8_backward(w, x, dY, A, B, 16.0)  # noqa: E731
+    call(), back()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for fn in (call, back):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(fn())
+        graphs.append(gr)
+    for k in range(4):
+        x.copy_(_rows(g, T, K))
+        dY.copy_(_rows(g, T, N))
+        want = [call(), back()]
+        torch.cuda.synchronize()
+        for gr in graphs:
+            gr.replay()
+        q.qlora_fp8_forward(_weight(g, 64, 64), _rows(g, 5, 64), None, None, 1.0)
+        torch.cuda.synchronize()
+        for a, b in zip(want, outs):
+            for s, t in zip(a, b):
+                assert torch.equal(s, t), k
