@@ -9,8 +9,179 @@
 // operand: a lane then holds one token (one xs) and four consecutive outputs.
 #include "fp8.h"
 #include "kernels.h"
+#include "tiles.h"
 
 namespace qlora {
+
+// ---------------------------------------------------------------------------
+// The tiled kernel: 256 outputs x 256 tokens per workgroup of eight waves, each
+// 128 outputs x 64 tokens; K advances by one scale block of 128. Both operands'
+// tiles go from memory straight into LDS (two tiles of each, step k + 1 on its
+// way during step k), as do the step's 256 token scales.
+// ---------------------------------------------------------------------------
+constexpr int kTileN = 256, kTileT = 256, kStep = 128;
+constexpr int kWaveN = 128, kWaveT = 64;
+constexpr int kOperand = kTileN * kStep;              // bytes of one operand's tile
+constexpr int kStage = 2 * kOperand + kTileT * 4;     // weight tile, token tile, token scales
+constexpr size_t kFp8Lds = (size_t)2 * kStage;
+
+// One dword per lane from memory into LDS (lane L lands at M0 + 4 L).
+__device__ __forceinline__ void dma4_asm(const i32x4 &rs, uint32_t m0v, uint32_t voff, uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds"
+      :
+      : "s"(m0v), "v"(voff), "s"(rs), "s"(soff)
+      : "memory");
+}
+
+typedef __attribute__((address_space(3))) i32x2v lds_i32x2;
+
+template <bool TRANS, bool E5M2>
+__global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__ W, const float *__restrict__ ws,
+                                                     int N, int K, int ldw, int sld, const uint8_t *__restrict__ xq,
+                                                     const float *__restrict__ xs, int64_t T,
+                                                     const uint16_t *__restrict__ su, int rp,
+                                                     const uint16_t *__restrict__ L, int r, int gn, int gt,
+                                                     uint16_t *__restrict__ out) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const int wn = wave & 1, wt = wave >> 1;
+  const int tn = blockIdx.x % gn, tt = blockIdx.x / gn;
+  const int64_t n0 = (int64_t)tn * kTileN, t0 = (int64_t)tt * kTileT;
+  const int nb = (K + kStep - 1) / kStep;
+  const int rows_t = T - t0 < kTileT ? (int)(T - t0) : kTileT;
+  const int rows_n = N - n0 < kTileN ? (int)(N - n0) : kTileN;
+
+  // copies: wave w, instruction q fills LDS bytes (4 w + q) KB of each operand's tile
+  const i32x4 xr = rsrc_words(xq + t0 * K, (int64_t)rows_t * K);
+  const i32x4 sr = rsrc_words(xs + t0 * nb, (int64_t)rows_t * nb * 4);
+  const i32x4 wr0 = rsrc_words(W + n0 * (TRANS ? 1 : (int64_t)ldw), TRANS ? 0 : (int64_t)rows_n * ldw);
+  uint32_t xv[4], wv[4];
+  int xc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int row = 8 * (4 * wave + q) + (lane >> 3);
+    xc[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+    xv[q] = (uint32_t)(row * K + xc[q]);
+    if constexpr (TRANS) {
+      const int k = 4 * (4 * wave + q) + (lane >> 4);
+      wv[q] = (uint32_t)(k * ldw + 16 * ((lane & 15) ^ ((k & 7) | (((k >> 4) & 1) << 3))));
+    } else {
+      wv[q] = (uint32_t)(row * ldw + xc[q]);
+    }
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  auto copy = [&](int b) {
+    const uint32_t base = lds0 + (uint32_t)(b & 1) * kStage;
+    const int k0 = b * kStep;
+    const bool cut = k0 + kStep > K;
+    i32x4 wr = wr0;
+    if constexpr (TRANS) {
+      const int left = K - k0 < kStep ? K - k0 : kStep;
+      wr = rsrc_words(W + (int64_t)k0 * ldw + n0, (int64_t)left * ldw - n0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = !cut || k0 + xc[q] < K;  // a chunk of 16 is whole or outside: K % 16 == 0
+      dma16_asm(xr, base + kOperand + 1024u * (uint32_t)(4 * wave + q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
+      if constexpr (TRANS)
+        dma16_asm(wr, base + 1024u * (uint32_t)(4 * wave + q), wv[q], 0u);
+      else
+        dma16_asm(wr, base + 1024u * (uint32_t)(4 * wave + q), in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
+    }
+    if (wave < 4)
+      dma4_asm(sr, base + 2 * kOperand + 256u * (uint32_t)wave, (uint32_t)((wave * 64 + lane) * nb + b) * 4u, 0u);
+  };
+
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int sw = (li >> 1) & 7;
+  const uint32_t frag = (uint32_t)(li * 128 + ((g ^ sw) << 4));
+  uint32_t tr[8];
+  if constexpr (TRANS) {
+    const uint32_t f = (uint32_t)((li >> 1) | ((g & 1) << 3));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      tr[i] = (uint32_t)((16 * g + (li >> 1)) * 256) + ((((uint32_t)(wn * 8 + i)) ^ f) << 4) + (uint32_t)(li & 1) * 8u;
+  }
+  const float *wsp = ws + (TRANS ? (n0 / 128 + wn) : (n0 / 128 + wn) * sld);
+  const bool have_n = n0 + wn * kWaveN < N;  // (a wave past the last column has no scale to read)
+
+  copy(0);
+  for (int b = 0; b < nb; ++b) {
+    wait_barrier<0>();
+    if (b + 1 < nb) copy(b + 1);
+    const uint8_t *st = smem + (size_t)(b & 1) * kStage;
+    const uint8_t *xt = st + kOperand + wt * (kWaveT * kStep), *wtile = st + (TRANS ? 0 : wn * (kWaveN * kStep));
+    const float wsc = have_n ? wsp[TRANS ? (int64_t)b * sld : b] : 0.f;
+    i32x8 xf[4];
+    float sc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      xf[j] = join8(ld16(xt + j * 2048 + frag), ld16(xt + j * 2048 + (frag ^ 64u)));
+      sc[j] = reinterpret_cast<const float *>(st + 2 * kOperand)[wt * kWaveT + j * 16 + li] * wsc;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      i32x8 wf;
+      if constexpr (TRANS) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const i32x2v v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (lds_i32x2 *)(wtile + tr[i] + (q & 1) * 2048 + (q >> 1) * 16384));
+          wf[2 * q] = v[0];
+          wf[2 * q + 1] = v[1];
+        }
+      } else {
+        wf = join8(ld16(wtile + i * 2048 + frag), ld16(wtile + i * 2048 + (frag ^ 64u)));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 p = mfma_fp8<E5M2>(wf, xf[j], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[j], acc[i][j][e]);
+      }
+    }
+  }
+
+  // the adapter term: rank columns in steps of 32, operands from memory
+  const int64_t nw = n0 + wn * kWaveN, tw = t0 + wt * kWaveT;
+  for (int k = 8 * g; k < r + 8 * g; k += 32) {
+    u32x4 sf[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sf[j] = u32x4{0, 0, 0, 0};
+      if (k < r && tw + j * 16 + li < T) sf[j] = ld16(su + (tw + j * 16 + li) * rp + k);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u32x4 lf = {0, 0, 0, 0};
+      if (k < r && nw + i * 16 + li < N) lf = ld16(L + (nw + i * 16 + li) * r + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = mfma16(lf, sf[j], acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t t = tw + j * 16 + li;
+    if (t < T) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t n = nw + i * 16 + 4 * g;
+        if (n < N)
+          *reinterpret_cast<u32x2 *>(out + t * N + n) =
+              u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+      }
+    }
+  }
+}
 
 // One wave per 16 x 16 outputs, operands straight from memory.
 template <bool TRANS, bool E5M2>
@@ -64,6 +235,25 @@ hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, 
                               const uint16_t *L, int r, uint16_t *out, hipStream_t st) {
   const int64_t N = trans ? d_in : d_out, K = trans ? d_out : d_in;
   const int64_t sld = (d_in + 127) / 128;
+  if (T > 16) {
+    auto *k = trans ? (e5m2 ? k_fp8_gemm<true, true> : k_fp8_gemm<true, false>)
+                    : (e5m2 ? k_fp8_gemm<false, true> : k_fp8_gemm<false, false>);
+    static DeviceOnce once;
+    const hipError_t e = once.run(current_device(), [] {
+      for (auto *f : {k_fp8_gemm<true, true>, k_fp8_gemm<true, false>, k_fp8_gemm<false, true>, k_fp8_gemm<false, false>}) {
+        const hipError_t s = hipFuncSetAttribute(reinterpret_cast<const void *>(f),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFp8Lds);
+        if (s != hipSuccess) return s;
+      }
+      return hipSuccess;
+    });
+    if (e != hipSuccess) return e;
+    const int64_t gn = (N + kTileN - 1) / kTileN, gt = (T + kTileT - 1) / kTileT;
+    if (gn * gt >= (int64_t)1 << 31) return hipErrorInvalidValue;
+    k<<<dim3((unsigned)(gn * gt)), dim3(512), kFp8Lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su,
+                                                             rp, L, r, (int)gn, (int)gt, out);
+    return hipGetLastError();
+  }
   const int64_t blocks = (N / 16) * ((T + 15) / 16);
   if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(64);
