@@ -21,9 +21,11 @@ namespace qlora {
 // ---------------------------------------------------------------------------
 constexpr int kTileN = 256, kTileT = 256, kStep = 128;
 constexpr int kWaveN = 128, kWaveT = 64;
+constexpr int kDown = 4;
 constexpr int kOperand = kTileN * kStep;              // bytes of one operand's tile
-constexpr int kStage = 2 * kOperand + kTileT * 4;     // weight tile, token tile, token scales
-constexpr size_t kFp8Lds = (size_t)2 * kStage;
+constexpr int kStage = 2 * kOperand;                  // weight tile, token tile
+constexpr int kScales = kTileT * 16;                  // four steps' token scales
+constexpr size_t kFp8Lds = (size_t)2 * kStage + 2 * kScales;
 
 // One dword per lane from memory into LDS (lane L lands at M0 + 4 L).
 __device__ __forceinline__ void dma4_asm(const i32x4 &rs, uint32_t m0v, uint32_t voff, uint32_t soff) {
@@ -49,7 +51,13 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
   const int wn = wave & 1, wt = wave >> 1;
-  const int tn = blockIdx.x % gn, tt = blockIdx.x / gn;
+  // The workgroups of one XCD (blockIdx % 8) take a contiguous share of the tiles in an order that walks down kDown
+  // token tiles before the next column, so that the 32 tiles it holds at once read 4 token tiles and 8 weight tiles.
+  const int tiles = gn * gt, share = tiles / 8, extra = tiles % 8, xcd = blockIdx.x % 8;
+  const int seq = xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+  const int band = seq / (kDown * gn), in_band = seq - band * kDown * gn;
+  const int down = gt - band * kDown < kDown ? gt - band * kDown : kDown;
+  const int tn = in_band / down, tt = band * kDown + in_band % down;
   const int64_t n0 = (int64_t)tn * kTileN, t0 = (int64_t)tt * kTileT;
   const int nb = (K + kStep - 1) / kStep;
   const int rows_t = T - t0 < kTileT ? (int)(T - t0) : kTileT;
@@ -60,40 +68,52 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   const i32x4 sr = rsrc_words(xs + t0 * nb, (int64_t)rows_t * nb * 4);
   const i32x4 wr0 = rsrc_words(W + n0 * (TRANS ? 1 : (int64_t)ldw), TRANS ? 0 : (int64_t)rows_n * ldw);
   uint32_t xv[4], wv[4];
-  int xc[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = 8 * (4 * wave + q) + (lane >> 3);
-    xc[q] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-    xv[q] = (uint32_t)(row * K + xc[q]);
+    const int c = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+    xv[q] = (uint32_t)(row * K + c);
     if constexpr (TRANS) {
       const int k = 4 * (4 * wave + q) + (lane >> 4);
       wv[q] = (uint32_t)(k * ldw + 16 * ((lane & 15) ^ ((k & 7) | (((k >> 4) & 1) << 3))));
     } else {
-      wv[q] = (uint32_t)(row * ldw + xc[q]);
+      wv[q] = (uint32_t)(row * ldw + c);
     }
   }
-  const uint32_t lds0 = lds_addr(smem);
-  auto copy = [&](int b) {
-    const uint32_t base = lds0 + (uint32_t)(b & 1) * kStage;
+  const uint32_t lds0 = lds_addr(smem) + 4096u * (uint32_t)wave;
+  // Column of the lane's chunk in pieces q = 0, 2 (and, 64 further on or back, q = 1, 3). A chunk is whole or past K
+  // (K % 16 == 0); past K it reads zeros, and so does every chunk of a step past the last.
+  const int c0 = 16 * ((lane & 7) ^ ((lane >> 4) & 7)), c1 = c0 ^ 64;
+  auto copy_x = [&](int b, int q) {
     const int k0 = b * kStep;
-    const bool cut = k0 + kStep > K;
-    i32x4 wr = wr0;
+    const bool in = k0 + ((q & 1) ? c1 : c0) < K;
+    dma16_asm(xr, lds0 + (uint32_t)((b & 1) * kStage + kOperand + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
+  };
+  auto copy_w = [&](int b, int q) {
+    const int k0 = b * kStep;
+    const uint32_t to = lds0 + (uint32_t)((b & 1) * kStage + 1024 * q);
     if constexpr (TRANS) {
       const int left = K - k0 < kStep ? K - k0 : kStep;
-      wr = rsrc_words(W + (int64_t)k0 * ldw + n0, (int64_t)left * ldw - n0);
+      dma16_asm(rsrc_words(W + (int64_t)k0 * ldw + n0, left > 0 ? (int64_t)left * ldw - n0 : 0), to, wv[q], 0u);
+    } else {
+      const bool in = k0 + ((q & 1) ? c1 : c0) < K;
+      dma16_asm(wr0, to, in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool in = !cut || k0 + xc[q] < K;  // a chunk of 16 is whole or outside: K % 16 == 0
-      dma16_asm(xr, base + kOperand + 1024u * (uint32_t)(4 * wave + q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
-      if constexpr (TRANS)
-        dma16_asm(wr, base + 1024u * (uint32_t)(4 * wave + q), wv[q], 0u);
-      else
-        dma16_asm(wr, base + 1024u * (uint32_t)(4 * wave + q), in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
+  };
+  // Token scales of four steps at once, 16 bytes per token; the last group starts early enough to end with the row.
+  // Rows of fewer than four scales: one step after another, tokens side by side.
+  const bool wide = nb >= 4;
+  const int s_tok = wide ? 16 : 4, s_step = wide ? 4 : kTileT * 4;
+  auto scale_start = [&](int group) { return wide && 4 * group + 4 > nb ? nb - 4 : 4 * group; };
+  auto copy_s = [&](int group) {
+    if (wave >= 4) return;
+    const uint32_t to = lds_addr(smem) + (uint32_t)(2 * kStage + (group & 1) * kScales);
+    const uint32_t at = (uint32_t)((wave * 64 + lane) * nb + scale_start(group)) * 4u;
+    if (wide) {
+      dma16_asm(sr, to + 1024u * (uint32_t)wave, at, 0u);
+    } else {
+      for (int k = 0; k < nb; ++k) dma4_asm(sr, to + (uint32_t)(k * s_step) + 256u * (uint32_t)wave, at + 4u * (uint32_t)k, 0u);
     }
-    if (wave < 4)
-      dma4_asm(sr, base + 2 * kOperand + 256u * (uint32_t)wave, (uint32_t)((wave * 64 + lane) * nb + b) * 4u, 0u);
   };
 
   f32x4 acc[8][4];
@@ -102,54 +122,118 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int sw = (li >> 1) & 7;
-  const uint32_t frag = (uint32_t)(li * 128 + ((g ^ sw) << 4));
-  uint32_t tr[8];
-  if constexpr (TRANS) {
-    const uint32_t f = (uint32_t)((li >> 1) | ((g & 1) << 3));
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      tr[i] = (uint32_t)((16 * g + (li >> 1)) * 256) + ((((uint32_t)(wn * 8 + i)) ^ f) << 4) + (uint32_t)(li & 1) * 8u;
-  }
-  const float *wsp = ws + (TRANS ? (n0 / 128 + wn) : (n0 / 128 + wn) * sld);
-  const bool have_n = n0 + wn * kWaveN < N;  // (a wave past the last column has no scale to read)
+  const uint32_t frag = (uint32_t)(li * 128 + ((g ^ ((li >> 1) & 7)) << 4));
+  // columns by transposing reads: lane l of 16 points at 8 bytes of row l / 2, and gets the 8 rows of column l
+  const uint32_t tr_row = (uint32_t)((16 * g + (li >> 1)) * 256 + (li & 1) * 8), tr_f = (uint32_t)((li >> 1) | ((g & 1) << 3));
+  // a wave past the last column reads the last block's scale: its results are not stored
+  const int64_t nblk = n0 / 128 + wn, nlast = (N - 1) / 128;
+  const float *wsp = ws + (nblk < nlast ? nblk : nlast) * (TRANS ? 1 : sld);
+  const int64_t wstep = TRANS ? sld : 1;
 
-  copy(0);
-  for (int b = 0; b < nb; ++b) {
-    wait_barrier<0>();
-    if (b + 1 < nb) copy(b + 1);
-    const uint8_t *st = smem + (size_t)(b & 1) * kStage;
-    const uint8_t *xt = st + kOperand + wt * (kWaveT * kStep), *wtile = st + (TRANS ? 0 : wn * (kWaveN * kStep));
-    const float wsc = have_n ? wsp[TRANS ? (int64_t)b * sld : b] : 0.f;
-    i32x8 xf[4];
-    float sc[4];
+  auto load_x = [&](const uint8_t *st, int j) {
+    const uint8_t *t = st + kOperand + wt * (kWaveT * kStep) + j * 2048;
+    return join8(ld16(t + frag), ld16(t + (frag ^ 64u)));
+  };
+  auto load_w = [&](const uint8_t *st, int i) {
+    if constexpr (TRANS) {
+      const uint8_t *t = st + tr_row + (((uint32_t)(wn * 8 + i) ^ tr_f) << 4);
+      i32x8 w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      xf[j] = join8(ld16(xt + j * 2048 + frag), ld16(xt + j * 2048 + (frag ^ 64u)));
-      sc[j] = reinterpret_cast<const float *>(st + 2 * kOperand)[wt * kWaveT + j * 16 + li] * wsc;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      i32x8 wf;
-      if constexpr (TRANS) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const i32x2v v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (lds_i32x2 *)(wtile + tr[i] + (q & 1) * 2048 + (q >> 1) * 16384));
-          wf[2 * q] = v[0];
-          wf[2 * q + 1] = v[1];
-        }
-      } else {
-        wf = join8(ld16(wtile + i * 2048 + frag), ld16(wtile + i * 2048 + (frag ^ 64u)));
+      for (int q = 0; q < 4; ++q) {
+        const i32x2v v =
+            __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(t + (q & 1) * 2048 + (q >> 1) * 16384));
+        w[2 * q] = v[0];
+        w[2 * q + 1] = v[1];
       }
+      return w;
+    } else {
+      const uint8_t *t = st + wn * (kWaveN * kStep) + i * 2048;
+      return join8(ld16(t + frag), ld16(t + (frag ^ 64u)));
+    }
+  };
+  auto load_s = [&](int b, int j) {
+    const uint8_t *t = smem + 2 * kStage + ((b >> 2) & 1) * kScales + (b - scale_start(b >> 2)) * s_step;
+    return *reinterpret_cast<const float *>(t + (wt * kWaveT + j * 16 + li) * s_tok);
+  };
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  i32x8 xf[4], w0;
+  float sc[4];
+  auto add = [&](const f32x4 &p, int i, int j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[j], acc[i][j][e]);
+    pin(acc[i][j]);  // (or the sums sink past the branches of the copy, and every product waits in registers)
+  };
+
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    copy_x(0, q);
+    copy_w(0, q);
+  }
+  copy_s(0);
+  wait_barrier<0>();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    copy_x(1, q);
+  }
+  float wsc = wsp[0];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    xf[j] = load_x(smem, j);
+    sc[j] = load_s(0, j) * wsc;
+  }
+  w0 = load_w(smem, 0);
+
+  for (int b = 0; b < nb; ++b) {
+    const uint8_t *st = smem + (size_t)(b & 1) * kStage, *next = smem + (size_t)((b & 1) ^ 1) * kStage;
+    i32x8 wf[3];
+    wf[0] = w0;
+    f32x4 p[2][4];
+    // outputs 16 i .. +15 of the wave, i = 0 .. 5: four products, the sums of the i before, the weights of the i after
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      wf[(i + 1) % 3] = load_w(st, i + 1);
+      if (i == 5) wf[1] = load_w(st, 7);
+      if (i == 3) wsc = wsp[(b + 1 < nb ? b + 1 : b) * wstep];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const f32x4 p = mfma_fp8<E5M2>(wf, xf[j], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[j], acc[i][j][e]);
+        p[i & 1][j] = mfma_fp8<E5M2>(wf[i % 3], xf[j], zero);
+        QLORA_SCHED_FENCE();
+        if (i < 2 && (j & 1)) copy_w(b + 1, 2 * i + (j >> 1));
+        if (i > 0) add(p[(i & 1) ^ 1][j], i - 1, j);
+        QLORA_SCHED_FENCE();
       }
     }
+    // every fragment of this step is in registers: the next step's tiles are awaited and the one after is sent for
+    // while i = 6, 7 are still to be multiplied
+    wait_barrier<0>();
+    if ((b & 3) == 0 && b + 4 < nb) copy_s((b >> 2) + 1);
+    QLORA_SCHED_FENCE();
+    f32x4 q6, q7;
+    float sn[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const f32x4 a6 = mfma_fp8<E5M2>(wf[0], xf[j], zero), a7 = mfma_fp8<E5M2>(wf[1], xf[j], zero);
+      QLORA_SCHED_FENCE();
+      copy_x(b + 2, j);
+      add(p[1][j], 5, j);
+      if (j > 0) {
+        add(q6, 6, j - 1);
+        add(q7, 7, j - 1);
+      }
+      q6 = a6;
+      q7 = a7;
+      xf[j] = load_x(next, j);
+      sn[j] = load_s(b + 1 < nb ? b + 1 : b, j);
+      if (j == 1) w0 = load_w(next, 0);
+      QLORA_SCHED_FENCE();
+    }
+    add(q6, 6, 3);
+    add(q7, 7, 3);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sc[j] = sn[j] * wsc;
   }
+
+  wait_vmem();  // no copy into LDS outlives the workgroup
 
   // the adapter term: rank columns in steps of 32, operands from memory
   const int64_t nw = n0 + wn * kWaveN, tw = t0 + wt * kWaveT;

@@ -22,6 +22,7 @@ typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 __device__ __forceinline__ void pin(uint32_t &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void pin(float &x) { asm volatile("" : "+v"(x)); }
 __device__ __forceinline__ void pin(u32x4 &x) { asm volatile("" : "+v"(x)); }
+__device__ __forceinline__ void pin(f32x4 &x) { asm volatile("" : "+v"(x)); }
 
 // Wait until at most N vector-memory operations of this wave are outstanding
 // and all of its LDS operations are done, then join the workgroup barrier. One
