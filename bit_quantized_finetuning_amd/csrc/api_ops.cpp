@@ -62,6 +62,8 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
     pf = std::max(pf, lora_wgrad_partial_floats(d_in, r, T));
     pf = std::max(pf, lora_wgrad_partial_floats(d_out, r, T));
   }
+  pf = std::max(pf, fp8_partial_floats(T, d_out, d_in, false));
+  pf = std::max(pf, fp8_partial_floats(T, d_in, d_out, true));
   L.partial = take(pf * 4);
   L.total = off;
   return L;
@@ -148,7 +150,8 @@ int qlora_fp8_forward(const qlora_fp8_weight *W, const uint8_t *xq, const float 
     if (e != hipSuccess) return QLORA_ERR_HIP;
   }
   return hip_status(launch_fp8_product(W->codes, W->scales, W->d_out, W->d_in, false, xq, xs, fmt == QLORA_E5M2, T, su,
-                                       rank_pad(r), B, r, h, stream));
+                                       rank_pad(r), B, r, h, at<float>(ws, L.partial), at<uint32_t>(ws, 0),
+                                       stream));
 }
 
 int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint16_t *dY, int fmt, int64_t T,
@@ -190,7 +193,7 @@ int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint1
     if (e == hipSuccess && r > 0) e = launch_transpose_bf16(A, r, d_in, at_, stream);
     if (e == hipSuccess)
       e = launch_fp8_product(W->codes, W->scales, d_out, d_in, true, q, qs, fmt == QLORA_E5M2, T, sv, rank_pad(r), at_,
-                             r, dX, stream);
+                             r, dX, partial, counters, stream);
     if (e != hipSuccess) return QLORA_ERR_HIP;
   }
   const bool wide = T >= kWideMinTokens;

@@ -7,24 +7,27 @@
 // it is scaled in float32 and added to the running float32 sum, so nothing is
 // rounded below 32 bits before the one rounding to bf16. The weight is the first
 // operand: a lane then holds one token (one xs) and four consecutive outputs.
+#include <cmath>
+
 #include "fp8.h"
+#include "host.h"
 #include "kernels.h"
 #include "tiles.h"
 
 namespace qlora {
 
 // ---------------------------------------------------------------------------
-// The tiled kernel: 256 outputs x 256 tokens per workgroup of eight waves, each
-// 128 outputs x 64 tokens; K advances by one scale block of 128. Both operands'
-// tiles go from memory straight into LDS (two tiles of each, step k + 1 on its
-// way during step k), as do the step's 256 token scales.
+// The large-tile kernel: 256 outputs x 64 MJ tokens per workgroup of eight waves,
+// each 128 outputs x 16 MJ tokens (MJ = 4 for whole batches, 3 and 2 where a
+// narrower tile leaves fewer compute units idle); K advances by one scale block
+// of 128. Both operands' tiles go from memory straight into LDS (two tiles of
+// each, step k + 1 on its way during step k), as do the token scales.
 // ---------------------------------------------------------------------------
-constexpr int kTileN = 256, kTileT = 256, kStep = 128;
-constexpr int kWaveN = 128, kWaveT = 64;
-constexpr int kDown = 4;
+constexpr int kTileN = 256, kStep = 128;
+constexpr int kWaveN = 128;
 constexpr int kOperand = kTileN * kStep;              // bytes of one operand's tile
 constexpr int kStage = 2 * kOperand;                  // weight tile, token tile
-constexpr int kScales = kTileT * 16;                  // four steps' token scales
+constexpr int kScales = 256 * 16;                     // four steps' token scales
 constexpr size_t kFp8Lds = (size_t)2 * kStage + 2 * kScales;
 
 // One dword per lane from memory into LDS (lane L lands at M0 + 4 L).
@@ -40,58 +43,77 @@ __device__ __forceinline__ void dma4_asm(const i32x4 &rs, uint32_t m0v, uint32_t
 
 typedef __attribute__((address_space(3))) i32x2v lds_i32x2;
 
-template <bool TRANS, bool E5M2>
+// Which tile (and K range) a workgroup takes. The workgroups of one XCD
+// (blockIdx % 8) take a contiguous share of the work in an order that walks
+// down kDown token tiles before the next K range or weight tile: what it holds
+// at once then shares its weight tiles kDown times and its token tiles among
+// the weight tiles (32 large tiles read 4 token tiles and 8 weight tiles), so
+// its L2 pulls each of them in once.
+constexpr int kDown = 4;
+struct WorkPlace {
+  int tn, tt, part;
+};
+__device__ __forceinline__ WorkPlace work_place(int gn, int gt, int parts) {
+  const int work = gn * gt * parts, share = work / 8, extra = work % 8, xcd = blockIdx.x % 8;
+  const int seq = xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+  const int band = seq / (kDown * gn * parts), in_band = seq - band * kDown * gn * parts;
+  const int down = gt - band * kDown < kDown ? gt - band * kDown : kDown;
+  const int col = in_band / down;
+  return WorkPlace{col / parts, band * kDown + in_band % down, col % parts};
+}
+
+template <bool TRANS, bool E5M2, int MJ>
 __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__ W, const float *__restrict__ ws,
                                                      int N, int K, int ldw, int sld, const uint8_t *__restrict__ xq,
                                                      const float *__restrict__ xs, int64_t T,
                                                      const uint16_t *__restrict__ su, int rp,
                                                      const uint16_t *__restrict__ L, int r, int gn, int gt,
                                                      uint16_t *__restrict__ out) {
+  constexpr int kTileT = 64 * MJ, kWaveT = 16 * MJ;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
   const int wn = wave & 1, wt = wave >> 1;
-  // The workgroups of one XCD (blockIdx % 8) take a contiguous share of the tiles in an order that walks down kDown
-  // token tiles before the next column, so that the 32 tiles it holds at once read 4 token tiles and 8 weight tiles.
-  const int tiles = gn * gt, share = tiles / 8, extra = tiles % 8, xcd = blockIdx.x % 8;
-  const int seq = xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
-  const int band = seq / (kDown * gn), in_band = seq - band * kDown * gn;
-  const int down = gt - band * kDown < kDown ? gt - band * kDown : kDown;
-  const int tn = in_band / down, tt = band * kDown + in_band % down;
+  const WorkPlace at = work_place(gn, gt, 1);
+  const int tn = at.tn, tt = at.tt;
   const int64_t n0 = (int64_t)tn * kTileN, t0 = (int64_t)tt * kTileT;
   const int nb = (K + kStep - 1) / kStep;
   const int rows_t = T - t0 < kTileT ? (int)(T - t0) : kTileT;
   const int rows_n = N - n0 < kTileN ? (int)(N - n0) : kTileN;
 
-  // copies: wave w, instruction q fills LDS bytes (4 w + q) KB of each operand's tile
+  // copies: wave w's piece q fills KB 4 w + q of the weight tile, KB MJ w + q of the token tile
   const i32x4 xr = rsrc_words(xq + t0 * K, (int64_t)rows_t * K);
   const i32x4 sr = rsrc_words(xs + t0 * nb, (int64_t)rows_t * nb * 4);
   const i32x4 wr0 = rsrc_words(W + n0 * (TRANS ? 1 : (int64_t)ldw), TRANS ? 0 : (int64_t)rows_n * ldw);
-  uint32_t xv[4], wv[4];
+  uint32_t xv[MJ], wv[4];
+#pragma unroll
+  for (int q = 0; q < MJ; ++q) {
+    const int row = 8 * (MJ * wave + q) + (lane >> 3);
+    xv[q] = (uint32_t)(row * K + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = 8 * (4 * wave + q) + (lane >> 3);
-    const int c = 16 * ((lane & 7) ^ ((row >> 1) & 7));
-    xv[q] = (uint32_t)(row * K + c);
     if constexpr (TRANS) {
       const int k = 4 * (4 * wave + q) + (lane >> 4);
       wv[q] = (uint32_t)(k * ldw + 16 * ((lane & 15) ^ ((k & 7) | (((k >> 4) & 1) << 3))));
     } else {
-      wv[q] = (uint32_t)(row * ldw + c);
+      wv[q] = (uint32_t)(row * ldw + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
     }
   }
-  const uint32_t lds0 = lds_addr(smem) + 4096u * (uint32_t)wave;
-  // Column of the lane's chunk in pieces q = 0, 2 (and, 64 further on or back, q = 1, 3). A chunk is whole or past K
+  const uint32_t lds_w = lds_addr(smem) + 4096u * (uint32_t)wave;
+  const uint32_t lds_x = lds_addr(smem) + kOperand + 1024u * MJ * (uint32_t)wave;
+  // Column of the lane's chunk in even KB of a tile and, 64 further on or back, in odd ones. A chunk is whole or past K
   // (K % 16 == 0); past K it reads zeros, and so does every chunk of a step past the last.
   const int c0 = 16 * ((lane & 7) ^ ((lane >> 4) & 7)), c1 = c0 ^ 64;
   auto copy_x = [&](int b, int q) {
     const int k0 = b * kStep;
-    const bool in = k0 + ((q & 1) ? c1 : c0) < K;
-    dma16_asm(xr, lds0 + (uint32_t)((b & 1) * kStage + kOperand + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
+    const bool in = k0 + (((MJ * wave + q) & 1) ? c1 : c0) < K;
+    dma16_asm(xr, lds_x + (uint32_t)((b & 1) * kStage + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
   };
   auto copy_w = [&](int b, int q) {
     const int k0 = b * kStep;
-    const uint32_t to = lds0 + (uint32_t)((b & 1) * kStage + 1024 * q);
+    const uint32_t to = lds_w + (uint32_t)((b & 1) * kStage + 1024 * q);
     if constexpr (TRANS) {
       const int left = K - k0 < kStep ? K - k0 : kStep;
       dma16_asm(rsrc_words(W + (int64_t)k0 * ldw + n0, left > 0 ? (int64_t)left * ldw - n0 : 0), to, wv[q], 0u);
@@ -106,7 +128,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   const int s_tok = wide ? 16 : 4, s_step = wide ? 4 : kTileT * 4;
   auto scale_start = [&](int group) { return wide && 4 * group + 4 > nb ? nb - 4 : 4 * group; };
   auto copy_s = [&](int group) {
-    if (wave >= 4) return;
+    if (wave >= MJ) return;
     const uint32_t to = lds_addr(smem) + (uint32_t)(2 * kStage + (group & 1) * kScales);
     const uint32_t at = (uint32_t)((wave * 64 + lane) * nb + scale_start(group)) * 4u;
     if (wide) {
@@ -116,11 +138,11 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     }
   };
 
-  f32x4 acc[8][4];
+  f32x4 acc[8][MJ];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const uint32_t frag = (uint32_t)(li * 128 + ((g ^ ((li >> 1) & 7)) << 4));
   // columns by transposing reads: lane l of 16 points at 8 bytes of row l / 2, and gets the 8 rows of column l
@@ -156,8 +178,8 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     return *reinterpret_cast<const float *>(t + (wt * kWaveT + j * 16 + li) * s_tok);
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  i32x8 xf[4], w0;
-  float sc[4];
+  i32x8 xf[MJ], w0;
+  float sc[MJ];
   auto add = [&](const f32x4 &p, int i, int j) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[j], acc[i][j][e]);
@@ -165,19 +187,16 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   };
 
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    copy_x(0, q);
-    copy_w(0, q);
-  }
+  for (int q = 0; q < 4; ++q) copy_w(0, q);
+#pragma unroll
+  for (int q = 0; q < MJ; ++q) copy_x(0, q);
   copy_s(0);
   wait_barrier<0>();
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    copy_x(1, q);
-  }
+  for (int q = 0; q < MJ; ++q) copy_x(1, q);
   float wsc = wsp[0];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < MJ; ++j) {
     xf[j] = load_x(smem, j);
     sc[j] = load_s(0, j) * wsc;
   }
@@ -187,7 +206,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     const uint8_t *st = smem + (size_t)(b & 1) * kStage, *next = smem + (size_t)((b & 1) ^ 1) * kStage;
     i32x8 wf[3];
     wf[0] = w0;
-    f32x4 p[2][4];
+    f32x4 p[2][MJ];
     // outputs 16 i .. +15 of the wave, i = 0 .. 5: four products, the sums of the i before, the weights of the i after
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
@@ -195,10 +214,11 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       if (i == 5) wf[1] = load_w(st, 7);
       if (i == 3) wsc = wsp[(b + 1 < nb ? b + 1 : b) * wstep];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < MJ; ++j) {
         p[i & 1][j] = mfma_fp8<E5M2>(wf[i % 3], xf[j], zero);
         QLORA_SCHED_FENCE();
-        if (i < 2 && (j & 1)) copy_w(b + 1, 2 * i + (j >> 1));
+        // (sent early in the step, two to a group: the last must land before its end)
+        if (MJ == 4 ? i < 2 && (j & 1) : i < 4 && j == 1) copy_w(b + 1, MJ == 4 ? 2 * i + (j >> 1) : i);
         if (i > 0) add(p[(i & 1) ^ 1][j], i - 1, j);
         QLORA_SCHED_FENCE();
       }
@@ -209,9 +229,9 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     if ((b & 3) == 0 && b + 4 < nb) copy_s((b >> 2) + 1);
     QLORA_SCHED_FENCE();
     f32x4 q6, q7;
-    float sn[4];
+    float sn[MJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < MJ; ++j) {
       const f32x4 a6 = mfma_fp8<E5M2>(wf[0], xf[j], zero), a7 = mfma_fp8<E5M2>(wf[1], xf[j], zero);
       QLORA_SCHED_FENCE();
       copy_x(b + 2, j);
@@ -227,10 +247,10 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       if (j == 1) w0 = load_w(next, 0);
       QLORA_SCHED_FENCE();
     }
-    add(q6, 6, 3);
-    add(q7, 7, 3);
+    add(q6, 6, MJ - 1);
+    add(q7, 7, MJ - 1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sc[j] = sn[j] * wsc;
+    for (int j = 0; j < MJ; ++j) sc[j] = sn[j] * wsc;
   }
 
   wait_vmem();  // no copy into LDS outlives the workgroup
@@ -238,9 +258,9 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   // the adapter term: rank columns in steps of 32, operands from memory
   const int64_t nw = n0 + wn * kWaveN, tw = t0 + wt * kWaveT;
   for (int k = 8 * g; k < r + 8 * g; k += 32) {
-    u32x4 sf[4];
+    u32x4 sf[MJ];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < MJ; ++j) {
       sf[j] = u32x4{0, 0, 0, 0};
       if (k < r && tw + j * 16 + li < T) sf[j] = ld16(su + (tw + j * 16 + li) * rp + k);
     }
@@ -249,11 +269,11 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       u32x4 lf = {0, 0, 0, 0};
       if (k < r && nw + i * 16 + li < N) lf = ld16(L + (nw + i * 16 + li) * r + k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = mfma16(lf, sf[j], acc[i][j]);
+      for (int j = 0; j < MJ; ++j) acc[i][j] = mfma16(lf, sf[j], acc[i][j]);
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < MJ; ++j) {
     const int64_t t = tw + j * 16 + li;
     if (t < T) {
 #pragma unroll
@@ -267,84 +287,365 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   }
 }
 
-// One wave per 16 x 16 outputs, operands straight from memory.
+// ---------------------------------------------------------------------------
+// The small-tile kernel, where the large tiles are too few to fill the chip:
+// 128 outputs x 64 tokens per workgroup of four waves (32 outputs x 64 tokens
+// each), three steps' tiles in LDS so that two are on their way during one, and
+// a K range per workgroup: `parts` workgroups share a tile, each stores its
+// float32 partial, and the last to arrive sums them in range order (so the
+// result does not depend on who is last) and writes the tile.
+// ---------------------------------------------------------------------------
+constexpr int kSmN = 128, kSmT = 64, kSmStages = 3;
+constexpr int kSmStage = (kSmN + kSmT) * kStep + kSmT * 4;  // weight tile, token tile, token scales
+constexpr size_t kSmLds = (size_t)kSmStages * kSmStage;
+
 template <bool TRANS, bool E5M2>
-__global__ __launch_bounds__(64) void k_fp8_product_simple(const uint8_t *__restrict__ W, const float *__restrict__ ws,
-                                                           int64_t N, int64_t K, int64_t ldw, int64_t lds_,
+__global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__restrict__ W, const float *__restrict__ ws,
+                                                           int N, int K, int ldw, int sld,
                                                            const uint8_t *__restrict__ xq, const float *__restrict__ xs,
                                                            int64_t T, const uint16_t *__restrict__ su, int rp,
-                                                           const uint16_t *__restrict__ L, int r,
+                                                           const uint16_t *__restrict__ L, int r, int gn, int gt, int parts,
+                                                           float *__restrict__ partial, uint32_t *__restrict__ counters,
                                                            uint16_t *__restrict__ out) {
-  const int lane = threadIdx.x, li = lane & 15, g = lane >> 4;
-  const int64_t nt = N / 16, n0 = (blockIdx.x % nt) * 16, t0 = (int64_t)(blockIdx.x / nt) * 16;
-  const int64_t nb = (K + 127) / 128;
-  const int64_t t = t0 + li < T ? t0 + li : T - 1;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t b = 0; b < nb; ++b) {
-    u32x4 wv[2] = {}, xv[2] = {};
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ uint32_t arrived;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const WorkPlace at = work_place(gn, gt, parts);
+  const int part = at.part, tile = at.tt * gn + at.tn;
+  const int64_t n0 = (int64_t)at.tn * kSmN, t0 = (int64_t)at.tt * kSmT;
+  const int nb = (K + kStep - 1) / kStep;
+  const int b0 = (int)((int64_t)nb * part / parts), b1 = (int)((int64_t)nb * (part + 1) / parts);
+  const int rows_t = T - t0 < kSmT ? (int)(T - t0) : kSmT;
+  const int rows_n = N - n0 < kSmN ? (int)(N - n0) : kSmN;
+
+  const i32x4 xr = rsrc_words(xq + t0 * K, (int64_t)rows_t * K);
+  const i32x4 sr = rsrc_words(xs + t0 * nb, (int64_t)rows_t * nb * 4);
+  const i32x4 wr0 = rsrc_words(W + n0 * (TRANS ? 1 : (int64_t)ldw), TRANS ? 0 : (int64_t)rows_n * ldw);
+  // wave w's pieces: KB 4 w .. +3 of the weight tile, KB 2 w, 2 w + 1 of the token tile
+  uint32_t xv[2], wv[4];
+  const int c0 = 16 * ((lane & 7) ^ ((lane >> 4) & 7)), c1 = c0 ^ 64;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t k = b * 128 + 64 * h + 16 * g;
-      if (k < K) {
-        xv[h] = ld16(xq + t * K + k);
-        if constexpr (TRANS) {
+  for (int q = 0; q < 4; ++q) {
+    const int row = 8 * (4 * wave + q) + (lane >> 3);
+    if constexpr (TRANS)
+      wv[q] = (uint32_t)(row * ldw + 16 * ((lane & 7) ^ (((row >> 1) & 3) | (((row >> 4) & 1) << 2))));
+    else
+      wv[q] = (uint32_t)(row * ldw + ((q & 1) ? c1 : c0));
+  }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) wv[h][i / 4] |= (uint32_t)W[(k + i) * ldw + n0 + li] << (8 * (i & 3));
-        } else {
-          wv[h] = ld16(W + (n0 + li) * ldw + k);
+  for (int q = 0; q < 2; ++q) xv[q] = (uint32_t)((8 * (2 * wave + q) + (lane >> 3)) * K + ((q & 1) ? c1 : c0));
+  // Copies of step b (six, and one more by wave 0); past b1 they read zeros, so the counts of the waits stay the same.
+  auto copy = [&](int b) {
+    const uint32_t base = lds_addr(smem) + (uint32_t)(b % kSmStages) * kSmStage;
+    const int k0 = b < b1 ? b * kStep : K;
+    i32x4 wr = wr0;
+    if constexpr (TRANS) {
+      const int left = K - k0 < kStep ? K - k0 : kStep;
+      wr = rsrc_words(W + (int64_t)k0 * ldw + n0, left > 0 ? (int64_t)left * ldw - n0 : 0);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = k0 + ((q & 1) ? c1 : c0) < K;
+      dma16_asm(wr, base + 1024u * (uint32_t)(4 * wave + q), TRANS ? wv[q] : in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
+      if (q < 2)
+        dma16_asm(xr, base + kSmN * kStep + 1024u * (uint32_t)(2 * wave + q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
+    }
+    if (wave == 0)
+      dma4_asm(sr, base + (kSmN + kSmT) * kStep, b < b1 ? (uint32_t)(lane * nb + b) * 4u : kOOB, 0u);
+  };
+
+  f32x4 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t frag = (uint32_t)(li * 128 + ((g ^ ((li >> 1) & 7)) << 4));
+  // transposing reads: rows of 128 bytes, chunk c of row k at c ^ ((k / 2 & 3) | (k / 16 & 1) << 2)
+  const uint32_t tr_row = (uint32_t)((16 * g + (li >> 1)) * 128 + (li & 1) * 8);
+  const uint32_t tr_f = (uint32_t)(((li >> 2) & 3) | ((g & 1) << 2));
+  const float *wsp = ws + (n0 / 128) * (TRANS ? 1 : sld);
+  const int64_t wstep = TRANS ? sld : 1;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+
+  copy(b0);
+  copy(b0 + 1);
+  float wsc = wsp[b0 * wstep];
+  for (int b = b0; b < b1; ++b) {
+    // step b's copies have landed (step b + 1's may be on their way) and every wave has read step b - 1
+    if (wave == 0)
+      wait_barrier<7>();
+    else
+      wait_barrier<6>();
+    copy(b + 2);
+    const uint8_t *st = smem + (size_t)(b % kSmStages) * kSmStage;
+    i32x8 wf[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (TRANS) {
+        const uint8_t *t = st + tr_row + (((uint32_t)(2 * wave + i) ^ tr_f) << 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const i32x2v v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2 *)(t + (q & 1) * 1024 + (q >> 1) * 8192));
+          wf[i][2 * q] = v[0];
+          wf[i][2 * q + 1] = v[1];
         }
+      } else {
+        const uint8_t *t = st + (2 * wave + i) * 2048;
+        wf[i] = join8(ld16(t + frag), ld16(t + (frag ^ 64u)));
       }
     }
-    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-    const f32x4 p = mfma_fp8<E5M2>(join8(wv[0], wv[1]), join8(xv[0], xv[1]), z);
-    const float s = xs[t * nb + b] * (TRANS ? ws[b * lds_ + n0 / 128] : ws[(n0 / 128) * lds_ + b]);
+    const uint8_t *xt = st + kSmN * kStep;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
-  }
-  for (int j = 0; j < r; j += 32) {
-    u32x4 a = {}, c = {};
-    const int k = j + 8 * g;
-    if (k < r) {
-      a = ld16(L + (n0 + li) * r + k);
-      c = ld16(su + t * rp + k);
+    for (int j = 0; j < 4; ++j) {
+      const i32x8 xf = join8(ld16(xt + j * 2048 + frag), ld16(xt + j * 2048 + (frag ^ 64u)));
+      const float sc = reinterpret_cast<const float *>(xt + kSmT * kStep)[j * 16 + li] * wsc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f32x4 p = mfma_fp8<E5M2>(wf[i], xf, zero);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc, acc[i][j][e]);
+      }
     }
-    acc = mfma16(a, c, acc);
+    wsc = wsp[(b + 1 < b1 ? b + 1 : b) * wstep];
   }
-  if (t0 + li < T)
-    *reinterpret_cast<u32x2 *>(out + t * N + n0 + 4 * g) = u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+  wait_vmem();  // no copy into LDS outlives the workgroup
+
+  const int64_t nw = n0 + 32 * wave;
+  if (parts > 1) {
+    // lane's 8 groups of four floats, [part][group][thread]: one 16-byte store each, whole lines per wave
+    float *mine = partial + ((int64_t)tile * parts + part) * (kSmN * kSmT);
+    const rsrc_t pr = make_rsrc(mine, kSmN * kSmT * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), pr,
+                                               (uint32_t)((i * 4 + j) * 256 + tid) * 16u, 0, 16);
+    wait_vmem();
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t *line = tile_counter(counters, tile);
+      arrived = add_dev_u32(line, 1u);
+      if (arrived == (uint32_t)(parts - 1)) st_dev_u32(line, 0u);
+    }
+    __syncthreads();
+    if (arrived != (uint32_t)(parts - 1)) return;
+    const rsrc_t all = make_rsrc(partial + (int64_t)tile * parts * (kSmN * kSmT), (int64_t)parts * kSmN * kSmT * 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = zero;
+    for (int p = 0; p < parts; p += 4) {  // four parts' loads in flight; past the last they read zeros
+      u32x4 v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[u][q] = bld16_dev(all, (uint32_t)(((p + u) * 8 + q) * 256 + tid) * 16u);
+      QLORA_SCHED_FENCE();
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q >> 2][q & 3] += __builtin_bit_cast(f32x4, v[u][q]);
+    }
+  }
+  for (int k = 8 * g; k < r + 8 * g; k += 32) {
+    u32x4 lf[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      lf[i] = u32x4{0, 0, 0, 0};
+      if (k < r && nw + i * 16 + li < N) lf[i] = ld16(L + (nw + i * 16 + li) * r + k);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 sf = {0, 0, 0, 0};
+      if (k < r && t0 + j * 16 + li < T) sf = ld16(su + (t0 + j * 16 + li) * rp + k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i][j] = mfma16(lf[i], sf, acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t t = t0 + j * 16 + li;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t n = nw + i * 16 + 4 * g;
+      if (t < T && n < N)
+        *reinterpret_cast<u32x2 *>(out + t * N + n) =
+            u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The weight-streaming kernel for at most 16 tokens: 16 outputs per workgroup,
+// its waves take turns at the K steps (together whole lines of every row), both
+// operands go from memory straight into the registers of the matrix
+// instruction, kAhead steps of a wave at a time, and the waves' sums meet in LDS.
+// The weight's bytes bound it.
+// ---------------------------------------------------------------------------
+constexpr int kStreamWaves = 8, kAhead = 4;
+
+template <bool E5M2>
+__global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t *__restrict__ W,
+                                                                  const float *__restrict__ ws, int N, int K,
+                                                                  const uint8_t *__restrict__ xq,
+                                                                  const float *__restrict__ xs, int T,
+                                                                  const uint16_t *__restrict__ su, int rp,
+                                                                  const uint16_t *__restrict__ L, int r,
+                                                                  uint16_t *__restrict__ out) {
+  __shared__ f32x4 red[kStreamWaves][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int nb = (K + kStep - 1) / kStep;
+  const rsrc_t wr = make_rsrc(W + n0 * K, (int64_t)16 * K), xr = make_rsrc(xq, (int64_t)T * K);
+  const rsrc_t sr = make_rsrc(xs, (int64_t)T * nb * 4), wsr = make_rsrc(ws + n0 / 128 * nb, (int64_t)nb * 4);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  const f32x4 zero = acc;
+  // operands of `kAhead` steps; steps past the last, chunks past K and tokens past T read zeros
+  u32x4 wv[kAhead][2], xv[kAhead][2];
+  float sx[kAhead], sw[kAhead];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int s = b + u * kStreamWaves, k = s * kStep + 16 * g;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool in = k + 64 * h < K;
+        wv[u][h] = bld16(wr, in ? (uint32_t)(li * K + k + 64 * h) : kOOB);
+        xv[u][h] = bld16(xr, in && li < T ? (uint32_t)(li * K + k + 64 * h) : kOOB);
+      }
+      sx[u] = __uint_as_float(bld32(sr, s < nb && li < T ? (uint32_t)(li * nb + s) * 4u : kOOB));
+      sw[u] = __uint_as_float(bld32(wsr, s < nb ? (uint32_t)s * 4u : kOOB));
+    }
+  };
+  for (int b = wave; b < nb; b += kStreamWaves * kAhead) {
+    load(b);
+    QLORA_SCHED_FENCE();  // every load of the batch is on its way before the first use
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const f32x4 p = mfma_fp8<E5M2>(join8(wv[u][0], wv[u][1]), join8(xv[u][0], xv[u][1]), zero);
+      const float s = sx[u] * sw[u];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], s, acc[e]);
+    }
+  }
+  if (wave == 0) {
+    for (int k = 8 * g; k < r + 8 * g; k += 32) {
+      u32x4 a = {0, 0, 0, 0}, c = {0, 0, 0, 0};
+      if (k < r) {
+        a = ld16(L + (n0 + li) * r + k);
+        if (li < T) c = ld16(su + (int64_t)li * rp + k);
+      }
+      acc = mfma16(a, c, acc);
+    }
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (tid < 64 && li < T) {
+#pragma unroll
+    for (int w = 1; w < kStreamWaves; ++w) acc += red[w][lane];
+    *reinterpret_cast<u32x2 *>(out + (int64_t)li * N + n0 + 4 * g) =
+        u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
+  }
+}
+
+namespace {
+
+// How a product is cut: the large-tile kernel with 64 mj tokens per tile, or (mj = 0) the small-tile kernel with
+// `parts` K ranges per tile.
+struct Fp8Plan {
+  int mj, parts;
+  int64_t gn, gt;
+};
+Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
+  const int64_t cus = device_cu_count(current_device()), nb = (K + kStep - 1) / kStep;
+  const double cus_d = (double)cus, steps = (double)nb;
+  Fp8Plan best{};
+  double least = INFINITY;
+  auto offer = [&](const Fp8Plan &p, double us) {
+    if (us < least) {
+      least = us;
+      best = p;
+    }
+  };
+  // Times in us from the measured steps. Large tiles: rounds of one workgroup per compute unit.
+  const int64_t gl = (N + kTileN - 1) / kTileN;
+  const double step_large[5] = {0, 0, 1.0, 1.2, 1.35}, ends_large[5] = {0, 0, 3.0, 6.0, 7.0};
+  for (int mj = 4; mj >= 2; --mj) {
+    const int64_t gt = (T + 64 * mj - 1) / (64 * mj), rounds = (gl * gt + cus - 1) / cus;
+    offer(Fp8Plan{mj, 1, gl, gt}, (double)rounds * (steps * step_large[mj] + ends_large[mj]));
+  }
+  // Small tiles: two workgroups share a compute unit; the last part's sum of the others
+  const int64_t gn = (N + kSmN - 1) / kSmN, gt = (T + kSmT - 1) / kSmT, tiles = gn * gt;
+  for (int parts = 1; parts <= 16; ++parts) {
+    if (parts > 1 && (tiles > kMaxTileCounters || tiles * parts > 4 * cus || nb < 2 * parts)) break;
+    const double fill = (double)(tiles * parts) / (2.0 * cus_d);
+    const double rounds = fill <= 1.0 ? 1.0 : std::ceil(2.0 * fill) / 2.0;
+    const double step = fill <= 0.5 ? (trans ? 0.7 : 0.5) : (trans ? 0.74 : 0.66) + 0.12 * std::min(1.0, 2.0 * fill - 1.0);
+    offer(Fp8Plan{0, parts, gn, gt}, rounds * (std::ceil(steps / parts) * step + 3.0) +
+                                         (parts > 1 ? 2.0 + 0.015 * (double)(tiles * parts) : 0.0));
+  }
+  return best;
+}
+
+template <typename F>
+hipError_t with_lds(F *f, DeviceOnce &once, size_t bytes) {
+  return once.run(current_device(), [&] {
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(f), hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
+}
+
+template <bool TRANS, bool E5M2>
+hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, const uint8_t *xq, const float *xs,
+                   int64_t T, const uint16_t *su, int rp, const uint16_t *L, int r, uint16_t *out, float *partial,
+                   uint32_t *counters, hipStream_t st) {
+  const int64_t N = TRANS ? d_in : d_out, K = TRANS ? d_out : d_in, sld = (d_in + 127) / 128;
+  if (!TRANS && T <= 16) {
+    k_fp8_stream<E5M2><<<dim3((unsigned)(N / 16)), dim3(64 * kStreamWaves), 0, st>>>(W, ws, (int)N, (int)K, xq, xs, (int)T,
+                                                                                    su, rp, L, r, out);
+    return hipGetLastError();
+  }
+  const Fp8Plan p = fp8_plan(T, N, K, TRANS);
+  if (p.gn * p.gt * p.parts >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)(p.gn * p.gt * p.parts));
+  if (p.mj) {
+    static DeviceOnce once[3];
+    auto large = [&](auto *k, DeviceOnce &o) {
+      const hipError_t e = with_lds(k, o, kFp8Lds);
+      if (e != hipSuccess) return e;
+      k<<<grid, dim3(512), kFp8Lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su, rp, L, r, (int)p.gn,
+                                          (int)p.gt, out);
+      return hipGetLastError();
+    };
+    if (p.mj == 4) return large(k_fp8_gemm<TRANS, E5M2, 4>, once[0]);
+    if (p.mj == 3) return large(k_fp8_gemm<TRANS, E5M2, 3>, once[1]);
+    return large(k_fp8_gemm<TRANS, E5M2, 2>, once[2]);
+  }
+  static DeviceOnce once;
+  auto *k = k_fp8_gemm_small<TRANS, E5M2>;
+  const hipError_t e = with_lds(k, once, kSmLds);
+  if (e != hipSuccess) return e;
+  k<<<grid, dim3(256), kSmLds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su, rp, L, r, (int)p.gn,
+                                     (int)p.gt, p.parts, partial, counters, out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
+  const Fp8Plan p = fp8_plan(T, N, K, trans);
+  return p.parts > 1 ? (size_t)(p.gn * p.gt * p.parts) * kSmN * kSmT : 0;
 }
 
 hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, bool trans,
                               const uint8_t *xq, const float *xs, bool e5m2, int64_t T, const uint16_t *su, int rp,
-                              const uint16_t *L, int r, uint16_t *out, hipStream_t st) {
-  const int64_t N = trans ? d_in : d_out, K = trans ? d_out : d_in;
-  const int64_t sld = (d_in + 127) / 128;
-  if (T > 16) {
-    auto *k = trans ? (e5m2 ? k_fp8_gemm<true, true> : k_fp8_gemm<true, false>)
-                    : (e5m2 ? k_fp8_gemm<false, true> : k_fp8_gemm<false, false>);
-    static DeviceOnce once;
-    const hipError_t e = once.run(current_device(), [] {
-      for (auto *f : {k_fp8_gemm<true, true>, k_fp8_gemm<true, false>, k_fp8_gemm<false, true>, k_fp8_gemm<false, false>}) {
-        const hipError_t s = hipFuncSetAttribute(reinterpret_cast<const void *>(f),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)kFp8Lds);
-        if (s != hipSuccess) return s;
-      }
-      return hipSuccess;
-    });
-    if (e != hipSuccess) return e;
-    const int64_t gn = (N + kTileN - 1) / kTileN, gt = (T + kTileT - 1) / kTileT;
-    if (gn * gt >= (int64_t)1 << 31) return hipErrorInvalidValue;
-    k<<<dim3((unsigned)(gn * gt)), dim3(512), kFp8Lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su,
-                                                             rp, L, r, (int)gn, (int)gt, out);
-    return hipGetLastError();
-  }
-  const int64_t blocks = (N / 16) * ((T + 15) / 16);
-  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks), block(64);
-  auto *k = trans ? (e5m2 ? k_fp8_product_simple<true, true> : k_fp8_product_simple<true, false>)
-                  : (e5m2 ? k_fp8_product_simple<false, true> : k_fp8_product_simple<false, false>);
-  k<<<grid, block, 0, st>>>(W, ws, N, K, d_in, sld, xq, xs, T, su, rp, L, r, out);
-  return hipGetLastError();
+                              const uint16_t *L, int r, uint16_t *out, float *partial, uint32_t *counters,
+                              hipStream_t st) {
+  auto *f = trans ? (e5m2 ? product<true, true> : product<true, false>)
+                  : (e5m2 ? product<false, true> : product<false, false>);
+  return f(W, ws, d_out, d_in, xq, xs, T, su, rp, L, r, out, partial, counters, st);
 }
 
 }  // namespace qlora

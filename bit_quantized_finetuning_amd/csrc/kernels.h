@@ -193,10 +193,12 @@ hipError_t launch_fp8_quantize_weight(const void *W, bool bf16_in, int64_t N, in
 
 // fp8_gemm.hip: out[T, N] = the block-scaled product of xq [T, K] with the e4m3 weight [d_out, d_in] (trans false:
 // N = d_out, K = d_in; true: the weight read by columns, N = d_in, K = d_out) + su L^T (su bf16 [T, rp], L bf16
-// [N, r]; r may be 0).
+// [N, r]; r may be 0). Uses `partial` (fp8_partial_floats) and `counters` (one tile_counter per output tile).
 hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, bool trans,
                               const uint8_t *xq, const float *xs, bool e5m2, int64_t T, const uint16_t *su, int rp,
-                              const uint16_t *L, int r, uint16_t *out, hipStream_t st);
+                              const uint16_t *L, int r, uint16_t *out, float *partial, uint32_t *counters,
+                              hipStream_t st);
+size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans);
 
 // rmsnorm.hip: row strides in elements; s, y, yq, dx and the partial sums are dense. partial: rmsnorm_partial_floats
 // floats when dw is wanted, else null.
