@@ -32,7 +32,7 @@ int64_t groups(int64_t d) { return ceil_div(d, QLORA_FP8_GROUP); }
 // first, as in every workspace; q8 and qs hold the rows quantized within the
 // call, lt the adapter matrix that is contracted over its other dimension.
 struct Fp8Layout {
-  size_t su, u, v, bt, lt, q8, qs, partial, total;
+  size_t ex, su, u, v, bt, lt, q8, qs, partial, total;
 };
 Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   Fp8Layout L{};
@@ -44,6 +44,7 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
     off = align256(off + bytes);
     return at;
   };
+  L.ex = take(T <= kFp8StreamTokens ? fp8_stream_exchange_bytes(rp) : 0);
   L.su = take((size_t)std::max<int64_t>(16, ceil_div(T, 16) * 16) * rp * 2);
   L.u = take((size_t)T * r * 4);
   L.v = take((size_t)T * r * 4);
@@ -143,6 +144,10 @@ int qlora_fp8_forward(const qlora_fp8_weight *W, const uint8_t *xq, const float 
     xq = q;
     xs = qs;
   }
+  if (T <= kFp8StreamTokens)
+    return hip_status(launch_fp8_stream(W->codes, W->scales, W->d_out, W->d_in, xq, xs, fmt == QLORA_E5M2, T, x, A, B, r,
+                                        rank_pad(r), r > 0 ? alpha / (float)r : 0.f, u_out, at<uint8_t>(ws, L.ex),
+                                        at<uint32_t>(ws, 0), h, stream));
   uint16_t *su = at<uint16_t>(ws, L.su);
   if (r > 0) {
     e = adapter_product(x, A, T, W->d_in, r, alpha / (float)r, u_out, su, at<float>(ws, L.partial), at<uint32_t>(ws, 0),

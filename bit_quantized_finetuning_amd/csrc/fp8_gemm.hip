@@ -483,24 +483,114 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 // operands go from memory straight into the registers of the matrix
 // instruction, kAhead steps of a wave at a time, and the waves' sums meet in LDS.
 // The weight's bytes bound it.
+//
+// The adapter's u = x A^T [T, r] is formed by the first workgroups of the same
+// launch (one per 16 ranks and slice of K; the last of the slices to arrive adds
+// them in order) while the others stream, and reaches them as pairs of
+// bf16(s u) that carry the launch's tag. A reader whose wait runs out (other
+// launches hold the compute units) forms what it misses itself, in the same
+// order of operations, so no wait needs another workgroup to run and the result
+// does not depend on who formed what. One compute unit reads about 28 GB/s from
+// memory, so a slice is kept to about 1024 of K (16 tokens, 4096 x 11008, r =
+// 64: 33.8 us with the whole of K in one workgroup, 19.8 with four slices,
+// 17.0 with eleven).
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8, kAhead = 4;
+constexpr int kUSlices = 16;  // at most
+constexpr int kSuPitch = QLORA_MAX_RANK + 8;
+
+struct StreamAdapter {
+  const uint16_t *x, *A, *B;
+  int r, rp, slices;
+  float scale;
+  float *u_out;
+  uint64_t *ex;    // [16][rp / 2] tagged pairs
+  float *partial;  // [rp / 16][slices][4][64] quarters
+  uint32_t *counters;
+};
+
+// Slice ks of K of u for ranks 16 rt .. +15, all tokens: lane l of wave 0 gets token l & 15, ranks 16 rt + 4 (l >> 4) + i.
+__device__ __forceinline__ f32x4 u_partial(const StreamAdapter &a, int K, int T, int rt, int ks, f32x4 (*red)[64]) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const int steps = (K + 31) / 32, sb = steps * ks / a.slices, se = steps * (ks + 1) / a.slices;
+  const rsrc_t ar = make_rsrc(a.A, (int64_t)a.r * K * 2), xr = make_rsrc(a.x, (int64_t)T * K * 2);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = sb + wave; s0 < se; s0 += kStreamWaves * kAhead) {
+    u32x4 av[kAhead], xv[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int s = s0 + u * kStreamWaves, k = s * 32 + 8 * g;
+      const bool in = s < se && k < K;
+      av[u] = bld16(ar, in && 16 * rt + li < a.r ? (uint32_t)(((16 * rt + li) * K + k) * 2) : kOOB);
+      xv[u] = bld16(xr, in && li < T ? (uint32_t)((li * K + k) * 2) : kOOB);
+    }
+    QLORA_SCHED_FENCE();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) acc = mfma16(av[u], xv[u], acc);
+  }
+  red[wave][lane] = acc;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < kStreamWaves; ++w) acc += red[w][lane];
+  }
+  __syncthreads();
+  return acc;
+}
 
 template <bool E5M2>
 __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t *__restrict__ W,
                                                                   const float *__restrict__ ws, int N, int K,
                                                                   const uint8_t *__restrict__ xq,
                                                                   const float *__restrict__ xs, int T,
-                                                                  const uint16_t *__restrict__ su, int rp,
-                                                                  const uint16_t *__restrict__ L, int r,
+                                                                  StreamAdapter ad, int producers,
                                                                   uint16_t *__restrict__ out) {
   __shared__ f32x4 red[kStreamWaves][64];
+  __shared__ __attribute__((aligned(16))) uint16_t su[16 * kSuPitch];
+  __shared__ uint32_t missing[QLORA_MAX_RANK / 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const uint32_t tag = producers ? launch_tag() : 0u;
+  if ((int)blockIdx.x < producers) {
+    const int rt = blockIdx.x / ad.slices, ks = blockIdx.x - rt * ad.slices;
+    f32x4 u = u_partial(ad, K, T, rt, ks, red);
+    if (wave != 0) return;
+    if (ad.slices > 1) {
+      float *mine = ad.partial + (int64_t)rt * ad.slices * 256 + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st_dev(mine + ks * 256 + 64 * i, u[i]);
+      wait_vmem();
+      uint32_t *line = tile_counter(ad.counters, rt);
+      uint32_t arrived = 0;
+      if (lane == 0) arrived = add_dev_u32(line, 1u);
+      if ((int)__builtin_amdgcn_readfirstlane(arrived) != ad.slices - 1) return;
+      if (lane == 0) st_dev_u32(line, 0u);
+      f32x4 q[kUSlices];
+#pragma unroll
+      for (int k = 0; k < kUSlices; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[k][i] = k < ad.slices ? ld_dev(mine + k * 256 + 64 * i) : 0.f;
+      QLORA_SCHED_FENCE();
+      u = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kUSlices; ++k) u += q[k];
+    }
+    if (li < T) {
+      const int j = 16 * rt + 4 * g;
+      uint64_t *to = ad.ex + (li * ad.rp + j) / 2;
+      st_dev_u64(to, ((uint64_t)pack_bf16x2(u[0] * ad.scale, u[1] * ad.scale) << 32) | tag);
+      st_dev_u64(to + 1, ((uint64_t)pack_bf16x2(u[2] * ad.scale, u[3] * ad.scale) << 32) | tag);
+      if (ad.u_out && j < ad.r) *reinterpret_cast<f32x4 *>(ad.u_out + li * ad.r + j) = u;
+    }
+    return;
+  }
+  const int64_t n0 = (int64_t)(blockIdx.x - producers) * 16;
   const int nb = (K + kStep - 1) / kStep;
   const rsrc_t wr = make_rsrc(W + n0 * K, (int64_t)16 * K), xr = make_rsrc(xq, (int64_t)T * K);
   const rsrc_t sr = make_rsrc(xs, (int64_t)T * nb * 4), wsr = make_rsrc(ws + n0 / 128 * nb, (int64_t)nb * 4);
+  u32x4 bv = {0, 0, 0, 0};
+  if (producers && 32 * wave + 8 * g < ad.r) bv = ld16(ad.B + (n0 + li) * ad.r + 32 * wave + 8 * g);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   const f32x4 zero = acc;
   // operands of `kAhead` steps; steps past the last, chunks past K and tokens past T read zeros
@@ -531,15 +621,42 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
       for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], s, acc[e]);
     }
   }
-  if (wave == 0) {
-    for (int k = 8 * g; k < r + 8 * g; k += 32) {
-      u32x4 a = {0, 0, 0, 0}, c = {0, 0, 0, 0};
-      if (k < r) {
-        a = ld16(L + (n0 + li) * r + k);
-        if (li < T) c = ld16(su + (int64_t)li * rp + k);
+  if (producers) {
+    const int tiles = ad.rp / 16, pairs = T * ad.rp / 2;
+    if (tid < tiles) missing[tid] = 0u;
+    __syncthreads();
+    const long long t0 = wall_clock64(), limit = wait_limit(ad.counters + kMaxCounters - 1);
+    for (int e = tid; e < pairs; e += 64 * kStreamWaves) {
+      const int t = e / (ad.rp / 2), j = 2 * (e - t * (ad.rp / 2));
+      for (;;) {
+        const uint64_t v = ld_dev_u64(ad.ex + e);
+        if ((uint32_t)v == tag) {
+          *reinterpret_cast<uint32_t *>(su + t * kSuPitch + j) = (uint32_t)(v >> 32);
+          break;
+        }
+        if (wall_clock64() - t0 > limit) {
+          missing[j / 16] = 1u;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
       }
-      acc = mfma16(a, c, acc);
     }
+    __syncthreads();
+    for (int rt = 0; rt < tiles; ++rt) {
+      if (!missing[rt]) continue;  // (the same for the whole workgroup)
+      if (tid == 0) add_dev_u32(ad.counters + kMaxCounters - 1, 1u);
+      f32x4 u = zero;
+      for (int ks = 0; ks < ad.slices; ++ks) u += u_partial(ad, K, T, rt, ks, red);
+      if (wave == 0 && li < T)
+        *reinterpret_cast<u32x2 *>(su + li * kSuPitch + 16 * rt + 4 * g) =
+            u32x2{pack_bf16x2(u[0] * ad.scale, u[1] * ad.scale), pack_bf16x2(u[2] * ad.scale, u[3] * ad.scale)};
+      __syncthreads();
+    }
+    // rank columns in steps of 32, one per wave (r <= 256)
+    u32x4 c = {0, 0, 0, 0};
+    const int k = 32 * wave + 8 * g;
+    if (k < ad.r && li < T) c = *reinterpret_cast<const u32x4 *>(su + li * kSuPitch + k);
+    acc = mfma16(bv, c, acc);
   }
   red[wave][lane] = acc;
   __syncthreads();
@@ -602,11 +719,6 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
                    int64_t T, const uint16_t *su, int rp, const uint16_t *L, int r, uint16_t *out, float *partial,
                    uint32_t *counters, hipStream_t st) {
   const int64_t N = TRANS ? d_in : d_out, K = TRANS ? d_out : d_in, sld = (d_in + 127) / 128;
-  if (!TRANS && T <= 16) {
-    k_fp8_stream<E5M2><<<dim3((unsigned)(N / 16)), dim3(64 * kStreamWaves), 0, st>>>(W, ws, (int)N, (int)K, xq, xs, (int)T,
-                                                                                    su, rp, L, r, out);
-    return hipGetLastError();
-  }
   const Fp8Plan p = fp8_plan(T, N, K, TRANS);
   if (p.gn * p.gt * p.parts >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)(p.gn * p.gt * p.parts));
@@ -637,6 +749,25 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
 size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   const Fp8Plan p = fp8_plan(T, N, K, trans);
   return p.parts > 1 ? (size_t)(p.gn * p.gt * p.parts) * kSmN * kSmT : 0;
+}
+
+// the tagged pairs, then the slices' partials
+size_t fp8_stream_exchange_bytes(int rp) { return (size_t)16 * rp / 2 * 8 + (size_t)rp / 16 * kUSlices * 256 * 4; }
+
+hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64_t K, const uint8_t *xq, const float *xs,
+                             bool e5m2, int64_t T, const uint16_t *x, const uint16_t *A, const uint16_t *B, int r, int rp,
+                             float scale, float *u_out, void *ex, uint32_t *counters, uint16_t *out,
+                             hipStream_t st) {
+  const int slices = (int)std::min<int64_t>(kUSlices, (K + 1023) / 1024);
+  const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, static_cast<uint64_t *>(ex),
+                         reinterpret_cast<float *>(static_cast<uint8_t *>(ex) + (size_t)16 * rp / 2 * 8), counters};
+  const int producers = r > 0 ? rp / 16 * slices : 0;
+  const dim3 grid((unsigned)(N / 16 + producers)), block(64 * kStreamWaves);
+  if (e5m2)
+    k_fp8_stream<true><<<grid, block, 0, st>>>(W, ws, (int)N, (int)K, xq, xs, (int)T, ad, producers, out);
+  else
+    k_fp8_stream<false><<<grid, block, 0, st>>>(W, ws, (int)N, (int)K, xq, xs, (int)T, ad, producers, out);
+  return hipGetLastError();
 }
 
 hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, bool trans,

@@ -199,6 +199,15 @@ hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, 
                               const uint16_t *L, int r, uint16_t *out, float *partial, uint32_t *counters,
                               hipStream_t st);
 size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans);
+// T <= kFp8StreamTokens, forward: out = the product + scale (x A^T) B^T in one launch (r = 0: without an adapter).
+// u_out (nullable) receives x A^T; ex: fp8_stream_exchange_bytes of scratch; counters: the workspace's counter region
+// (one tile_counter per 16 ranks; its last word counts the tiles that a reader formed itself).
+constexpr int64_t kFp8StreamTokens = 16;
+hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64_t K, const uint8_t *xq, const float *xs,
+                             bool e5m2, int64_t T, const uint16_t *x, const uint16_t *A, const uint16_t *B, int r, int rp,
+                             float scale, float *u_out, void *ex, uint32_t *counters, uint16_t *out,
+                             hipStream_t st);
+size_t fp8_stream_exchange_bytes(int rp);
 
 // rmsnorm.hip: row strides in elements; s, y, yq, dx and the partial sums are dense. partial: rmsnorm_partial_floats
 // floats when dw is wanted, else null.

@@ -318,3 +318,20 @@ def test_captured_calls(T):
         for a, b in zip(want, outs):
             for s, t in zip(a, b):
                 assert torch.equal(s, t), k
+
+
+@pytest.mark.parametrize("T,N,K,r", [(1, 512, 1040, 8), (5, 1024, 2064, 40), (16, 4096, 4096, 256)])
+def test_streaming_forward_without_its_producers(T, N, K, r):
+    """With the waits cut to one tick, readers that find a partial of x A^T missing form it themselves: the same bits."""
+    say(f"fp8 stream fallback T={T} {N}x{K} r={r}")
+    g = _gen("fallback", T)
+    w, x = _weight(g, N, K), _rows(g, T, K)
+    A, B = _adapter(g, N, K, r)
+    ws = torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, r), dtype=torch.uint8, device="cuda")
+    h, u = q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True, ws=ws)
+    q.qlora_workspace_set_wait_limit(ws, 1)
+    for _ in range(3):
+        h1, u1 = q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True, ws=ws)
+        assert torch.equal(h1, h) and torch.equal(u1, u)
+    say(f"    partials formed by readers: {q.qlora_workspace_fallbacks(ws)}")
+    q.qlora_workspace_set_wait_limit(ws, 0)
