@@ -47,6 +47,12 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
+try:
+    from . import _marshal  # native marshalling of the calls made most often (csrc/binding.cpp)
+except ImportError as e:
+    raise ImportError(f"{os.path.dirname(LIB_PATH)}/_marshal.so is not built ({e}); run "
+                      "`python -m bit_quantized_finetuning_amd.build`") from e
+
 
 class _Nf4Weight(ctypes.Structure):
     _fields_ = [("d_out", ctypes.c_int64), ("d_in", ctypes.c_int64), ("codes", ctypes.c_void_p),
@@ -689,6 +695,21 @@ def _groups(d: int) -> int:
     return -(-d // FP8_GROUP)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device index, as an integer
+
+
+def _done(answer, where: str):
+    """The results of a call that the native marshalling made; a status it got is raised."""
+    if type(answer) is int:
+        _check(answer, where)
+    return answer
+
+
+def _cached_ws(dev: int):
+    """The device's cached workspace for a native call (None while a graph is captured, see _call_ws)."""
+    return None if torch.cuda.is_current_stream_capturing() else _workspaces.get(("cuda", dev))
+
+
 def _on(dev):
     """The library launches on the current device: make `dev` current where it is not."""
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
@@ -793,8 +814,14 @@ def qlora_fp8_forward(w: Fp8Weight, x: torch.Tensor | None, A: torch.Tensor | No
     xq, xs: the 8-bit rows of a norm or of qlora_fp8_quantize_rows, in fmt; without them x (bf16 [T, d_in]) is
     quantized to fmt within the call. x itself is needed then, and for the adapter. u is float32 [T, r] when
     save_u or given, else None."""
-    _check_fp8_weight(w)
     f = _fmt(fmt)
+    if h is None and u is None and ws is None and w.codes.is_cuda:
+        dev = torch.cuda.current_device()
+        out = _marshal.fp8_forward(w.codes, w.scales, w.d_out, w.d_in, x, A, B, alpha, xq, xs, f, save_u,
+                                   _cached_ws(dev), dev, _raw_stream(dev))
+        if out is not None:
+            return _done(out, "qlora_fp8_forward")
+    _check_fp8_weight(w)
     if (xq is None) != (xs is None):
         raise ValueError("give both xq and xs, or neither")
     lead = x if x is not None else xq
@@ -839,8 +866,14 @@ def qlora_fp8_backward(w: Fp8Weight, x: torch.Tensor | None, dY: torch.Tensor, A
                        dA: torch.Tensor | None = None, dB: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """Returns (dX bf16 [T, d_in] | None, dA f32 [r, d_in] | None, dB f32 [d_out, r] | None); dY is quantized to fmt
     within the call for dX's product with the base, and used as it is for the adapter."""
-    _check_fp8_weight(w)
     f = _fmt(fmt)
+    if dX is None and dA is None and dB is None and ws is None and w.codes.is_cuda:
+        dev = torch.cuda.current_device()
+        out = _marshal.fp8_backward(w.codes, w.scales, w.d_out, w.d_in, x, dY, A, B, alpha, u_saved, need_dx, need_dA,
+                                    need_dB, f, _cached_ws(dev), dev, _raw_stream(dev))
+        if out is not None:
+            return _done(out, "qlora_fp8_backward")
+    _check_fp8_weight(w)
     if not torch.is_tensor(dY) or dY.dim() != 2 or dY.shape[0] < 1:
         raise ValueError("dY must be a 2-D [T >= 1, d_out] tensor")
     T = dY.shape[0]
@@ -920,6 +953,12 @@ def qlora_rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, r
     """s = x + residual (rounded to x's dtype); y = s / sqrt(mean(s^2) + eps) * weight over the rows of x [T, d]
     (float32 or bfloat16, any row stride). y comes in x's dtype (want_y) and / or as 8-bit rows with scales (fmt:
     torch.float8_e4m3fn or torch.float8_e5m2), as qlora_fp8_forward takes them."""
+    f = 0 if fmt is None else _fmt(fmt)
+    if torch.is_tensor(x) and x.is_cuda:
+        dev = torch.cuda.current_device()
+        out = _marshal.rmsnorm_forward(x, weight, residual, eps, want_y, f, save_rstd, dev, _raw_stream(dev))
+        if out is not None:
+            return RMSNormOut(*_done(out, "qlora_rmsnorm_forward"))
     dt = _float(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a 2-D [T, d] tensor")
@@ -929,7 +968,6 @@ def qlora_rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, r
     _rows(x, "x", x.dtype, T, d)
     _rows(residual, "residual", x.dtype, T, d)
     wd = _norm_weight(weight, d)
-    f = 0 if fmt is None else _fmt(fmt)
     if not want_y and fmt is None:
         raise ValueError("nothing to write: want_y is false and fmt is None")
     dev = x.device
@@ -952,6 +990,11 @@ def qlora_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
                            ds: torch.Tensor | None = None, need_dw: bool = False, ws: torch.Tensor | None = None):
     """Returns (dx, dw): dx in s's dtype is the gradient of x and of the residual; dw float32 [d] when need_dw. dy is
     the gradient of y, ds the one that reaches s past the norm (both in s's dtype, any row stride)."""
+    if ws is None and torch.is_tensor(s) and s.is_cuda:
+        dev = torch.cuda.current_device()
+        out = _marshal.rmsnorm_backward(dy, s, weight, rstd, ds, need_dw, dev, _raw_stream(dev))
+        if out is not None:
+            return _done(out, "qlora_rmsnorm_backward")
     dt = _float(s, "s")
     if s.dim() != 2:
         raise ValueError("s must be a 2-D [T, d] tensor")
@@ -1010,6 +1053,12 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     bits that depend on (seed, step, place) alone. max_norm: gradients are scaled to at most that global norm first,
     and a norm that is not finite leaves everything as it was; the norm is returned (float32 [1], on the device)."""
     grads, params = list(grads), list(params)
+    if ws is None and (max_norm is None or max_norm > 0) and torch.is_tensor(m) and m.is_cuda:
+        dev = torch.cuda.current_device()
+        out = _marshal.adamw_many(step, grads, params, m, v, m_scale, v_scale, master, lr, beta1, beta2, eps,
+                                  weight_decay, 0.0 if max_norm is None else max_norm, seed, norm, dev, _raw_stream(dev))
+        if out is not None:
+            return _done(out, "qlora_adamw_many")[0]
     count = len(grads)
     if len(params) != count:
         raise ValueError(f"{count} gradients but {len(params)} parameters")
