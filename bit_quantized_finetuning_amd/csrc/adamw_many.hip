@@ -27,17 +27,15 @@ namespace qlora {
 
 constexpr int kManyBlock = 256;
 
-// The job that block b of the launch belongs to (jobs without elements have no blocks).
+// The job that block b of the launch belongs to (jobs without elements have no
+// blocks): every lane compares two of the jobs' ends, so it takes one load's
+// time (a binary search takes seven, one after another).
 __device__ __forceinline__ int find_job(const ManyJobs &jobs, uint32_t b) {
-  int lo = 0, hi = jobs.count - 1;  // blk0[lo] <= b < blk0[hi + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (b < jobs.blk0[mid + 1])
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
+  static_assert(kManyJobs <= 128, "two ends per lane");
+  const int lane = threadIdx.x & 63;
+  const uint32_t e0 = lane < jobs.count ? jobs.blk0[lane + 1] : ~0u;
+  const uint32_t e1 = lane + 64 < jobs.count ? jobs.blk0[lane + 65] : ~0u;
+  return __popcll(__ballot(b >= e0)) + __popcll(__ballot(b >= e1));
 }
 
 // Four gradients at p, `left` of them inside the tensor.
@@ -94,20 +92,34 @@ __global__ __launch_bounds__(256) void k_grad_sq(ManyJobs jobs, double *__restri
   if (threadIdx.x == 0) partial[blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
-// out[0] = the norm, out[1] = the factor on the gradients (NaN: leave everything as it was)
-__global__ __launch_bounds__(256) void k_grad_norm(const double *__restrict__ partial, int n, float max_norm,
-                                                   float *__restrict__ norm_out, float *__restrict__ coef) {
-  __shared__ double red[4];
+// The norm from the workgroups' sums of squares, in every thread of a workgroup of 256.
+__device__ __forceinline__ float norm_of(const double *__restrict__ partial, int n, double *red) {
   double sum = 0.0;
-  for (int i = threadIdx.x; i < n; i += 256) sum += partial[i];
+  for (int i0 = threadIdx.x; i0 < n; i0 += 1024) {
+    double v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = i0 + 256 * u < n ? partial[i0 + 256 * u] : 0.0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum += v[u];
+  }
 #pragma unroll
   for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
+  return (float)sqrt(red[0] + red[1] + red[2] + red[3]);
+}
+// The factor on the gradients; NaN: leave everything as it was.
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+  return norm < INFINITY ? fminf(1.f, max_norm * (1.f / (norm + 1e-6f))) : NAN;
+}
+
+__global__ __launch_bounds__(256) void k_grad_norm(const double *__restrict__ partial, int n, float max_norm,
+                                                   float *__restrict__ norm_out, float *__restrict__ coef) {
+  __shared__ double red[4];
+  const float norm = norm_of(partial, n, red);
   if (threadIdx.x == 0) {
-    const float norm = (float)sqrt(red[0] + red[1] + red[2] + red[3]);
     *norm_out = norm;
-    *coef = norm < INFINITY ? fminf(1.f, max_norm * (1.f / (norm + 1e-6f))) : NAN;
+    *coef = clip_factor(norm, max_norm);
   }
 }
 
@@ -270,10 +282,18 @@ __device__ __forceinline__ void step_block(const G *grad, void *param, int64_t l
 
 // a.c2 holds sqrt(1 - b2^t) here.
 template <typename G, bool BITS8, bool MASTER>
-__global__ __launch_bounds__(256) void k_adamw_many(ManyJobs jobs, ManyState st, AdamWArgs a,
-                                                    const float *__restrict__ coef_p, uint32_t key) {
+__global__ __launch_bounds__(256) void k_adamw_many(ManyJobs jobs, ManyState st, AdamWArgs a, ManyClip clip,
+                                                    uint32_t key) {
   using P = typename std::conditional<MASTER, uint16_t, float>::type;
-  const float coef = coef_p ? *coef_p : 1.f;
+  __shared__ double red[4];
+  float coef = 1.f;
+  if (clip.partial) {
+    const float norm = norm_of(clip.partial, clip.n, red);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *clip.norm = norm;
+    coef = clip_factor(norm, clip.max_norm);
+  } else if (clip.coef) {
+    coef = *clip.coef;
+  }
   if (coef != coef) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t total = jobs.blk0[jobs.count], nw = gridDim.x * 4;
@@ -318,9 +338,9 @@ hipError_t launch_grad_norm(const double *partial, int n, float max_norm, float 
 }
 
 hipError_t launch_adamw_many(const ManyJobs &jobs, const ManyState &s, bool grad_bf16, bool bits8, bool master,
-                             const AdamWArgs &a, const float *coef, uint32_t key, hipStream_t st) {
+                             const AdamWArgs &a, const ManyClip &clip, uint32_t key, hipStream_t st) {
   const dim3 grid(many_grid(jobs.blk0[jobs.count])), block(256);
-#define QLORA_MANY(G, B8, M) k_adamw_many<G, B8, M><<<grid, block, 0, st>>>(jobs, s, a, coef, key)
+#define QLORA_MANY(G, B8, M) k_adamw_many<G, B8, M><<<grid, block, 0, st>>>(jobs, s, a, clip, key)
   if (grad_bf16) {
     if (bits8)
       master ? QLORA_MANY(uint16_t, true, true) : QLORA_MANY(uint16_t, true, false);

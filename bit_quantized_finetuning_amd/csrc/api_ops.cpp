@@ -346,6 +346,7 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
     }
     return i;
   };
+  ManyClip factor{};
   if (clip) {
     int n = 0;
     for (int32_t i = 0; i < count;) {
@@ -355,13 +356,20 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
       if (launch_grad_sq(t, grad_dtype == QLORA_BF16, partial + n, &wgs, stream) != hipSuccess) return QLORA_ERR_HIP;
       n += wgs;
     }
-    if (launch_grad_norm(partial, n, max_norm, norm, coef, stream) != hipSuccess) return QLORA_ERR_HIP;
+    // One launch's sums are few enough for every workgroup of the step to add itself, which spares a launch (the
+    // adapters of one decoder layer: NORMFUSED); those of several are added once.
+    if (count <= kManyJobs && n > 0) {
+      factor = ManyClip{nullptr, partial, norm, n, max_norm};
+    } else {
+      if (launch_grad_norm(partial, n, max_norm, norm, coef, stream) != hipSuccess) return QLORA_ERR_HIP;
+      factor.coef = coef;
+    }
   }
   ManyState st{state->m, state->v, state->m_scale, state->v_scale, state->master, 0};
   for (int32_t i = 0; i < count;) {
     i = fill(i);
     if (t.blk0[t.count] == 0) continue;
-    if (launch_adamw_many(t, st, grad_dtype == QLORA_BF16, bits8, master, a, coef, key, stream) != hipSuccess)
+    if (launch_adamw_many(t, st, grad_dtype == QLORA_BF16, bits8, master, a, factor, key, stream) != hipSuccess)
       return QLORA_ERR_HIP;
     st.base += t.blk0[t.count];
   }

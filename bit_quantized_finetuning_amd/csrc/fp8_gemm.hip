@@ -53,13 +53,16 @@ constexpr int kDown = 4;
 struct WorkPlace {
   int tn, tt, part;
 };
-__device__ __forceinline__ WorkPlace work_place(int gn, int gt, int parts) {
-  const int work = gn * gt * parts, share = work / 8, extra = work % 8, xcd = blockIdx.x % 8;
-  const int seq = xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8;
+__device__ __forceinline__ WorkPlace tile_place(int seq, int gn, int gt, int parts) {
   const int band = seq / (kDown * gn * parts), in_band = seq - band * kDown * gn * parts;
   const int down = gt - band * kDown < kDown ? gt - band * kDown : kDown;
   const int col = in_band / down;
   return WorkPlace{col / parts, band * kDown + in_band % down, col % parts};
+}
+// blockIdx of `work` workgroups -> its place
+__device__ __forceinline__ WorkPlace work_place(int work, int gn, int gt, int parts) {
+  const int share = work / 8, extra = work % 8, xcd = blockIdx.x % 8;
+  return tile_place(xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8, gn, gt, parts);
 }
 
 template <bool TRANS, bool E5M2, int MJ>
@@ -67,17 +70,25 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
                                                      int N, int K, int ldw, int sld, const uint8_t *__restrict__ xq,
                                                      const float *__restrict__ xs, int64_t T,
                                                      const uint16_t *__restrict__ su, int rp,
-                                                     const uint16_t *__restrict__ L, int r, int gn, int gt,
-                                                     uint16_t *__restrict__ out) {
+                                                     const uint16_t *__restrict__ L, int r, int gn, int gt, int full,
+                                                     int parts, float *__restrict__ partial,
+                                                     uint32_t *__restrict__ counters, uint16_t *__restrict__ out) {
   constexpr int kTileT = 64 * MJ, kWaveT = 16 * MJ;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
   const int wn = wave & 1, wt = wave >> 1;
-  const WorkPlace at = work_place(gn, gt, 1);
+  // tiles 0 .. full - 1 (in work_place's order) run whole, the others in `parts` K ranges of whole scale groups
+  const bool cut = (int)blockIdx.x >= full;
+  const int rest = gn * gt - full, e = (int)blockIdx.x - full;
+  const int tail = cut ? e % rest : 0, part = cut ? e / rest : 0;
+  const WorkPlace at = cut ? tile_place(full + tail, gn, gt, 1) : work_place(full, gn, gt, 1);
   const int tn = at.tn, tt = at.tt;
   const int64_t n0 = (int64_t)tn * kTileN, t0 = (int64_t)tt * kTileT;
-  const int nb = (K + kStep - 1) / kStep;
+  const int nb = (K + kStep - 1) / kStep, nb4 = (nb + 3) / 4;
+  const int b0 = cut ? 4 * (nb4 * part / parts) : 0;
+  const int b1 = cut && part + 1 < parts ? 4 * (nb4 * (part + 1) / parts) : nb;
+  const int klim = b1 * kStep < K ? b1 * kStep : K;
   const int rows_t = T - t0 < kTileT ? (int)(T - t0) : kTileT;
   const int rows_n = N - n0 < kTileN ? (int)(N - n0) : kTileN;
 
@@ -103,22 +114,22 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   }
   const uint32_t lds_w = lds_addr(smem) + 4096u * (uint32_t)wave;
   const uint32_t lds_x = lds_addr(smem) + kOperand + 1024u * MJ * (uint32_t)wave;
-  // Column of the lane's chunk in even KB of a tile and, 64 further on or back, in odd ones. A chunk is whole or past K
-  // (K % 16 == 0); past K it reads zeros, and so does every chunk of a step past the last.
+  // Column of the lane's chunk in even KB of a tile and, 64 further on or back, in odd ones. A chunk is whole or past
+  // the range's end (K % 16 == 0); there it reads zeros, and so does every chunk of a step past the last.
   const int c0 = 16 * ((lane & 7) ^ ((lane >> 4) & 7)), c1 = c0 ^ 64;
   auto copy_x = [&](int b, int q) {
     const int k0 = b * kStep;
-    const bool in = k0 + (((MJ * wave + q) & 1) ? c1 : c0) < K;
+    const bool in = k0 + (((MJ * wave + q) & 1) ? c1 : c0) < klim;
     dma16_asm(xr, lds_x + (uint32_t)((b & 1) * kStage + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
   };
   auto copy_w = [&](int b, int q) {
     const int k0 = b * kStep;
     const uint32_t to = lds_w + (uint32_t)((b & 1) * kStage + 1024 * q);
     if constexpr (TRANS) {
-      const int left = K - k0 < kStep ? K - k0 : kStep;
+      const int left = klim - k0 < kStep ? klim - k0 : kStep;
       dma16_asm(rsrc_words(W + (int64_t)k0 * ldw + n0, left > 0 ? (int64_t)left * ldw - n0 : 0), to, wv[q], 0u);
     } else {
-      const bool in = k0 + ((q & 1) ? c1 : c0) < K;
+      const bool in = k0 + ((q & 1) ? c1 : c0) < klim;
       dma16_asm(wr0, to, in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
     }
   };
@@ -187,22 +198,23 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   };
 
 #pragma unroll
-  for (int q = 0; q < 4; ++q) copy_w(0, q);
+  for (int q = 0; q < 4; ++q) copy_w(b0, q);
 #pragma unroll
-  for (int q = 0; q < MJ; ++q) copy_x(0, q);
-  copy_s(0);
+  for (int q = 0; q < MJ; ++q) copy_x(b0, q);
+  copy_s(b0 >> 2);
   wait_barrier<0>();
 #pragma unroll
-  for (int q = 0; q < MJ; ++q) copy_x(1, q);
-  float wsc = wsp[0];
+  for (int q = 0; q < MJ; ++q) copy_x(b0 + 1, q);
+  float wsc = wsp[b0 * wstep];
+  const uint8_t *first = smem + (size_t)(b0 & 1) * kStage;
 #pragma unroll
   for (int j = 0; j < MJ; ++j) {
-    xf[j] = load_x(smem, j);
-    sc[j] = load_s(0, j) * wsc;
+    xf[j] = load_x(first, j);
+    sc[j] = load_s(b0, j) * wsc;
   }
-  w0 = load_w(smem, 0);
+  w0 = load_w(first, 0);
 
-  for (int b = 0; b < nb; ++b) {
+  for (int b = b0; b < b1; ++b) {
     const uint8_t *st = smem + (size_t)(b & 1) * kStage, *next = smem + (size_t)((b & 1) ^ 1) * kStage;
     i32x8 wf[3];
     wf[0] = w0;
@@ -212,7 +224,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     for (int i = 0; i < 6; ++i) {
       wf[(i + 1) % 3] = load_w(st, i + 1);
       if (i == 5) wf[1] = load_w(st, 7);
-      if (i == 3) wsc = wsp[(b + 1 < nb ? b + 1 : b) * wstep];
+      if (i == 3) wsc = wsp[(b + 1 < b1 ? b + 1 : b) * wstep];
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
         p[i & 1][j] = mfma_fp8<E5M2>(wf[i % 3], xf[j], zero);
@@ -226,7 +238,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     // every fragment of this step is in registers: the next step's tiles are awaited and the one after is sent for
     // while i = 6, 7 are still to be multiplied
     wait_barrier<0>();
-    if ((b & 3) == 0 && b + 4 < nb) copy_s((b >> 2) + 1);
+    if ((b & 3) == 0 && b + 4 < b1) copy_s((b >> 2) + 1);
     QLORA_SCHED_FENCE();
     f32x4 q6, q7;
     float sn[MJ];
@@ -243,7 +255,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       q6 = a6;
       q7 = a7;
       xf[j] = load_x(next, j);
-      sn[j] = load_s(b + 1 < nb ? b + 1 : b, j);
+      sn[j] = load_s(b + 1 < b1 ? b + 1 : b, j);
       if (j == 1) w0 = load_w(next, 0);
       QLORA_SCHED_FENCE();
     }
@@ -254,6 +266,53 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   }
 
   wait_vmem();  // no copy into LDS outlives the workgroup
+
+  if (cut) {
+    // [part][group of four floats][thread]: one 16-byte store each, whole lines per wave
+    constexpr int kGroups = 8 * MJ, kPart = kGroups * 512 * 16;
+    float *mine = partial + ((int64_t)tail * parts + part) * (kPart / 4);
+    const rsrc_t pr = make_rsrc(mine, kPart);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < MJ; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), pr,
+                                               (uint32_t)((i * MJ + j) * 512 + tid) * 16u, 0, 16);
+    wait_vmem();
+    __syncthreads();
+    uint32_t *arrived = reinterpret_cast<uint32_t *>(smem);
+    if (tid == 0) {
+      uint32_t *line = tile_counter(counters, tail);
+      *arrived = add_dev_u32(line, 1u);
+      if (*arrived == (uint32_t)(parts - 1)) st_dev_u32(line, 0u);
+    }
+    __syncthreads();
+    if (*arrived != (uint32_t)(parts - 1)) return;
+    // the last to arrive adds the ranges in order, its own from its registers
+    const rsrc_t all = make_rsrc(partial + (int64_t)tail * parts * (kPart / 4), (int64_t)parts * kPart);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      f32x4 sum[2 * MJ];
+#pragma unroll
+      for (int q = 0; q < 2 * MJ; ++q) sum[q] = zero;
+      for (int p = 0; p < parts; ++p) {
+        u32x4 v[2 * MJ];
+        if (p != part) {
+#pragma unroll
+          for (int q = 0; q < 2 * MJ; ++q)
+            v[q] = bld16_dev(all, (uint32_t)((p * kGroups + i * MJ + q) * 512 + tid) * 16u);
+          QLORA_SCHED_FENCE();
+#pragma unroll
+          for (int q = 0; q < 2 * MJ; ++q) sum[q] += __builtin_bit_cast(f32x4, v[q]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2 * MJ; ++q) sum[q] += acc[i + q / MJ][q % MJ];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 2 * MJ; ++q) acc[i + q / MJ][q % MJ] = sum[q];
+    }
+  }
 
   // the adapter term: rank columns in steps of 32, operands from memory
   const int64_t nw = n0 + wn * kWaveN, tw = t0 + wt * kWaveT;
@@ -311,7 +370,7 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
   __shared__ uint32_t arrived;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
-  const WorkPlace at = work_place(gn, gt, parts);
+  const WorkPlace at = work_place(gn * gt * parts, gn, gt, parts);
   const int part = at.part, tile = at.tt * gn + at.tn;
   const int64_t n0 = (int64_t)at.tn * kSmN, t0 = (int64_t)at.tt * kSmT;
   const int nb = (K + kStep - 1) / kStep;
@@ -670,11 +729,12 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
 
 namespace {
 
-// How a product is cut: the large-tile kernel with 64 mj tokens per tile, or (mj = 0) the small-tile kernel with
-// `parts` K ranges per tile.
+// How a product is cut: the large-tile kernel with 64 mj tokens per tile, its first `full` tiles whole and the others
+// in `parts` K ranges; or (mj = 0) the small-tile kernel with `parts` K ranges for every tile.
 struct Fp8Plan {
   int mj, parts;
-  int64_t gn, gt;
+  int64_t gn, gt, full;
+  int64_t workgroups() const { return full + (gn * gt - full) * parts; }
 };
 Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
   const int64_t cus = device_cu_count(current_device()), nb = (K + kStep - 1) / kStep;
@@ -687,12 +747,20 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
       best = p;
     }
   };
-  // Times in us from the measured steps. Large tiles: rounds of one workgroup per compute unit.
+  // Times in us from the measured steps. Large tiles: rounds of one workgroup per compute unit; where the last round
+  // would leave half of them idle, its tiles are cut into K ranges, whose partial tiles are written once more
+  // and read by one workgroup (45 bytes a ns).
   const int64_t gl = (N + kTileN - 1) / kTileN;
   const double step_large[5] = {0, 0, 1.0, 1.2, 1.35}, ends_large[5] = {0, 0, 3.0, 6.0, 7.0};
   for (int mj = 4; mj >= 2; --mj) {
-    const int64_t gt = (T + 64 * mj - 1) / (64 * mj), rounds = (gl * gt + cus - 1) / cus;
-    offer(Fp8Plan{mj, 1, gl, gt}, (double)rounds * (steps * step_large[mj] + ends_large[mj]));
+    const int64_t gt = (T + 64 * mj - 1) / (64 * mj), tiles = gl * gt, rest = tiles % cus;
+    const double round = steps * step_large[mj] + ends_large[mj];
+    offer(Fp8Plan{mj, 1, gl, gt, tiles}, (double)((tiles + cus - 1) / cus) * round);
+    const int parts = rest ? (int)std::min<int64_t>(std::min<int64_t>(cus / rest, 8), nb / 8) : 1;
+    if (parts > 1 && rest <= kMaxTileCounters)
+      offer(Fp8Plan{mj, parts, gl, gt, tiles - rest},
+            (double)(tiles / cus) * round + steps / parts * step_large[mj] + ends_large[mj] + 2.0 +
+                1.45 * mj * (parts - 1) + 0.008 * mj * (double)(rest * parts));
   }
   // Small tiles: two workgroups share a compute unit; the last part's sum of the others
   const int64_t gn = (N + kSmN - 1) / kSmN, gt = (T + kSmT - 1) / kSmT, tiles = gn * gt;
@@ -700,9 +768,9 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
     if (parts > 1 && (tiles > kMaxTileCounters || tiles * parts > 4 * cus || nb < 2 * parts)) break;
     const double fill = (double)(tiles * parts) / (2.0 * cus_d);
     const double rounds = fill <= 1.0 ? 1.0 : std::ceil(2.0 * fill) / 2.0;
-    const double step = fill <= 0.5 ? (trans ? 0.7 : 0.5) : (trans ? 0.74 : 0.66) + 0.12 * std::min(1.0, 2.0 * fill - 1.0);
-    offer(Fp8Plan{0, parts, gn, gt}, rounds * (std::ceil(steps / parts) * step + 3.0) +
-                                         (parts > 1 ? 2.0 + 0.015 * (double)(tiles * parts) : 0.0));
+    const double step = fill <= 0.5 ? (trans ? 0.7 : 0.5) : (trans ? 0.70 : 0.66) + 0.12 * std::min(1.0, 2.0 * fill - 1.0);
+    offer(Fp8Plan{0, parts, gn, gt, 0}, rounds * (std::ceil(steps / parts) * step + 3.0) +
+                                         (parts > 1 ? 2.0 + 0.012 * (double)(tiles * parts) : 0.0));
   }
   return best;
 }
@@ -720,15 +788,15 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
                    uint32_t *counters, hipStream_t st) {
   const int64_t N = TRANS ? d_in : d_out, K = TRANS ? d_out : d_in, sld = (d_in + 127) / 128;
   const Fp8Plan p = fp8_plan(T, N, K, TRANS);
-  if (p.gn * p.gt * p.parts >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)(p.gn * p.gt * p.parts));
+  if (p.workgroups() >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)p.workgroups());
   if (p.mj) {
     static DeviceOnce once[3];
     auto large = [&](auto *k, DeviceOnce &o) {
       const hipError_t e = with_lds(k, o, kFp8Lds);
       if (e != hipSuccess) return e;
       k<<<grid, dim3(512), kFp8Lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su, rp, L, r, (int)p.gn,
-                                          (int)p.gt, out);
+                                          (int)p.gt, (int)p.full, p.parts, partial, counters, out);
       return hipGetLastError();
     };
     if (p.mj == 4) return large(k_fp8_gemm<TRANS, E5M2, 4>, once[0]);
@@ -748,7 +816,8 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
 
 size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   const Fp8Plan p = fp8_plan(T, N, K, trans);
-  return p.parts > 1 ? (size_t)(p.gn * p.gt * p.parts) * kSmN * kSmT : 0;
+  if (p.parts == 1) return 0;
+  return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? kTileN * 64 * p.mj : kSmN * kSmT);
 }
 
 // the tagged pairs, then the slices' partials

@@ -253,10 +253,20 @@ struct ManyState {
   float *m_scale, *v_scale, *master;
   int64_t base;
 };
-static_assert(sizeof(ManyJobs) + sizeof(ManyState) + sizeof(AdamWArgs) + 16 <= 4096, "kernel arguments");
+// The factor on the gradients: 1, or *coef, or formed by every workgroup from the n sums of squares in `partial`
+// (which also writes *norm).
+struct ManyClip {
+  const float *coef;
+  const double *partial;
+  float *norm;
+  int n;
+  float max_norm;
+};
+static_assert(sizeof(ManyJobs) + sizeof(ManyState) + sizeof(AdamWArgs) + sizeof(ManyClip) + 16 <= 4096,
+              "kernel arguments");
 hipError_t launch_grad_sq(const ManyJobs &jobs, bool bf16, double *partial, int *wgs, hipStream_t st);
 hipError_t launch_grad_norm(const double *partial, int n, float max_norm, float *norm, float *coef, hipStream_t st);
 hipError_t launch_adamw_many(const ManyJobs &jobs, const ManyState &s, bool grad_bf16, bool bits8, bool master,
-                             const AdamWArgs &a, const float *coef, uint32_t key, hipStream_t st);
+                             const AdamWArgs &a, const ManyClip &clip, uint32_t key, hipStream_t st);
 
 }  // namespace qlora

@@ -105,6 +105,22 @@ SHAPES = [  # T, d_out, d_in, r
 ]
 
 
+# tokens, outputs, contracted width: large tiles of 256, 192 and 128 tokens, whole and with their last round cut into
+# K ranges
+LARGE = [(776, 5168, 288), (3166, 2608, 256), (2964, 4560, 256), (201, 13520, 4720), (1031, 15136, 2704),
+         (1781, 13696, 3344), (1204, 14208, 4800)]
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+def test_forward_large(T, N, K):
+    test_forward(T, N, K, 16, True)
+
+
+@pytest.mark.parametrize("T,K,N", LARGE)
+def test_backward_large(T, N, K):
+    test_backward(T, N, K, 16)
+
+
 @pytest.mark.parametrize("given", [True, False])
 @pytest.mark.parametrize("T,N,K,r", SHAPES)
 def test_forward(T, N, K, r, given):
