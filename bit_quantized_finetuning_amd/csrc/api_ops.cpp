@@ -278,11 +278,11 @@ int qlora_rmsnorm_backward(const void *dy, int64_t ldy, const void *s, int64_t l
 // ---------------------------------------------------------------------------
 // AdamW over many tensors
 // ---------------------------------------------------------------------------
-static int64_t many_launches(int64_t count) { return std::max<int64_t>(1, ceil_div(count, kManyJobs)); }
-
+// The factor, then kManyPartials sums of squares per launch (a tensor without a gradient ends a launch, so there may
+// be one for every other tensor).
 size_t qlora_adamw_many_workspace_bytes(int32_t count) {
   if (count < 0) return 0;
-  return align256(sizeof(float)) + (size_t)many_launches(count) * kManyPartials * sizeof(double);
+  return align256(sizeof(float)) + (size_t)std::max<int32_t>(1, count) * kManyPartials * sizeof(double);
 }
 
 int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlora_adamw_job *jobs, int32_t count,
@@ -300,7 +300,7 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
   int64_t blocks = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (jobs[i].n < 0 || jobs[i].n >= (int64_t)1 << 38) return QLORA_ERR_SHAPE;
-    if (jobs[i].n > 0 && (!jobs[i].grad || !jobs[i].param)) return QLORA_ERR_NULL;
+    if (jobs[i].n > 0 && !jobs[i].param) return QLORA_ERR_NULL;
     if (!aligned16(jobs[i].grad) || !aligned16(jobs[i].param)) return QLORA_ERR_ALIGN;
     blocks += ceil_div(jobs[i].n, QLORA_ADAMW_BLOCK);
     if (blocks >= (int64_t)1 << 31) return QLORA_ERR_SHAPE;
@@ -332,33 +332,45 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
   float *coef = clip ? static_cast<float *>(ws) : nullptr;
   double *partial = clip ? at<double>(ws, align256(sizeof(float))) : nullptr;
 
-  // the tensors of one launch, from `i` on; returns the first one after them
+  // The tensors of one launch, from `i` on: a run of tensors that have a gradient. Returns the first one after them;
+  // `base` is the place of their first block in the state arrays, `next` that of the block after them.
   ManyJobs t;
+  int64_t base = 0, next = 0;
   auto fill = [&](int32_t i) {
     t.count = 0;
     t.blk0[0] = 0;
+    base = next;
     for (; i < count && t.count < kManyJobs; ++i) {
+      const int64_t blocks = ceil_div(jobs[i].n, QLORA_ADAMW_BLOCK);
+      if (blocks > 0 && !jobs[i].grad) {
+        if (t.count > 0) break;  // it ends the run
+        next += blocks;
+        base = next;
+        continue;
+      }
+      next += blocks;
       t.grad[t.count] = jobs[i].grad;
       t.param[t.count] = jobs[i].param;
       t.n[t.count] = jobs[i].n;
-      t.blk0[t.count + 1] = t.blk0[t.count] + (uint32_t)ceil_div(jobs[i].n, QLORA_ADAMW_BLOCK);
+      t.blk0[t.count + 1] = t.blk0[t.count] + (uint32_t)blocks;
       ++t.count;
     }
     return i;
   };
   ManyClip factor{};
   if (clip) {
-    int n = 0;
+    int n = 0, launches = 0;
     for (int32_t i = 0; i < count;) {
       i = fill(i);
       if (t.blk0[t.count] == 0) continue;
+      ++launches;
       int wgs = 0;
       if (launch_grad_sq(t, grad_dtype == QLORA_BF16, partial + n, &wgs, stream) != hipSuccess) return QLORA_ERR_HIP;
       n += wgs;
     }
     // One launch's sums are few enough for every workgroup of the step to add itself, which spares a launch (the
     // adapters of one decoder layer: NORMFUSED); those of several are added once.
-    if (count <= kManyJobs && n > 0) {
+    if (launches == 1) {
       factor = ManyClip{nullptr, partial, norm, n, max_norm};
     } else {
       if (launch_grad_norm(partial, n, max_norm, norm, coef, stream) != hipSuccess) return QLORA_ERR_HIP;
@@ -366,12 +378,13 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
     }
   }
   ManyState st{state->m, state->v, state->m_scale, state->v_scale, state->master, 0};
+  next = 0;
   for (int32_t i = 0; i < count;) {
     i = fill(i);
     if (t.blk0[t.count] == 0) continue;
+    st.base = base;
     if (launch_adamw_many(t, st, grad_dtype == QLORA_BF16, bits8, master, a, factor, key, stream) != hipSuccess)
       return QLORA_ERR_HIP;
-    st.base += t.blk0[t.count];
   }
   return QLORA_OK;
 }

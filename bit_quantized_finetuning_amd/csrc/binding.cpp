@@ -282,17 +282,20 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
   int64_t total = 0;
   for (Py_ssize_t i = 0; i < count; ++i) {
     PyObject *go = PyList_GET_ITEM(a[1], i), *po = PyList_GET_ITEM(a[2], i);
-    need(THPVariable_Check(go) && THPVariable_Check(po));
-    const Tensor &g = THPVariable_Unpack(go), &p = THPVariable_Unpack(po);
-    const int gt = float_type(g), pt = float_type(p);
-    if (i == 0) {
-      gd = gt;
-      pd = pt;
-    }
+    need(THPVariable_Check(po));
+    const Tensor &p = THPVariable_Unpack(po);
+    const Tensor g = tensor(go);  // None: the tensor is left as it is
+    const int pt = float_type(p);
+    if (pd < 0) pd = pt;
     const int64_t size = p.numel();
-    need(gt == gd && pt == pd && g.numel() == size && g.is_contiguous() && p.is_contiguous());
+    need(pt == pd && p.is_contiguous());
+    if (g.defined()) {
+      const int gt = float_type(g);
+      if (gd < 0) gd = gt;
+      need(gt == gd && g.numel() == size && g.is_contiguous());
+    }
     on(dev, {&g, &p});
-    jobs[(size_t)i] = qlora_adamw_job{g.data_ptr(), p.data_ptr(), size};
+    jobs[(size_t)i] = qlora_adamw_job{ptr(g), p.data_ptr(), size};
     if (size) {
       const uintptr_t at = reinterpret_cast<uintptr_t>(p.data_ptr());
       spans.emplace_back(at, at + (uintptr_t)size * p.element_size());
@@ -301,6 +304,7 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
   }
   std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i) need(spans[i - 1].second <= spans[i].first);
+  if (gd < 0) gd = QLORA_F32;
   const bool bits8 = m.scalar_type() == at::kFloat8_e4m3fn;
   need(bits8 || m.scalar_type() == at::kFloat);
   is(m, m.scalar_type(), {total});

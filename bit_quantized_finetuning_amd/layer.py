@@ -18,6 +18,12 @@ gradients on each adapter parameter, as `param.grad_fp32` (summed over
 backward passes while `param.grad` accumulates, started afresh when
 `param.grad` is None); PagedAdamW steps on those.
 
+The frozen base can also be kept in 8-bit floating point (base="fp8": e4m3 with one scale per 128 x 128 block,
+qlora_fp8_quantize): the forward multiplies 8-bit rows of the input with it, the backward 8-bit rows of the upstream
+gradient (the adapter's products stay in bf16). The input's 8-bit rows come from the norm before the projection
+(QLoRARMSNorm writes them beside its bf16 rows) or are formed within the call; gradients pass straight through that
+rounding.
+
 The modules compute in bf16 only: a dtype cast of a module (`.to(dtype)`,
 `.half()`, `.float()`) leaves its quantized buffers and adapter parameters as
 they are, and only a device move applies to them. With a frozen A (LoRA-FA: "8GB, 12GB, 16GB, 24GB GPU에서 몇 B
@@ -61,6 +67,60 @@ class QLoRALinearFunction(torch.autograd.Function):
                 None)
 
 
+class Fp8LinearFunction(torch.autograd.Function):
+    """As QLoRALinearFunction over an 8-bit base; xq, xs: x's 8-bit rows and scales, or None."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, w: q.Fp8Weight, alpha: float, recompute_u: bool = False, grad_sink=None, xq=None, xs=None,
+                grad_fmt=q.E4M3):
+        r = 0 if A is None else A.shape[0]
+        keep_u = r > 0 and not recompute_u
+        h, u = q.qlora_fp8_forward(w, x, A, B, alpha, xq=xq, xs=xs, fmt=q.E4M3 if xq is None else xq.dtype, save_u=keep_u)
+        keep_x = A is not None and (A.requires_grad or not keep_u)
+        ctx.w, ctx.alpha, ctx.r, ctx.grad_sink, ctx.grad_fmt = w, alpha, r, grad_sink, grad_fmt
+        ctx.save_for_backward(x if keep_x else None, A, B, u)
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        x, A, B, u = ctx.saved_tensors
+        dX, dA, dB = q.qlora_fp8_backward(ctx.w, x, dh.contiguous(), A, B, ctx.alpha, u_saved=u,
+                                          need_dx=ctx.needs_input_grad[0],
+                                          need_dA=ctx.r > 0 and ctx.needs_input_grad[1],
+                                          need_dB=ctx.r > 0 and ctx.needs_input_grad[2], fmt=ctx.grad_fmt)
+        if ctx.grad_sink is not None:
+            ctx.grad_sink(dA, dB)
+        return (dX, None if dA is None else dA.to(A.dtype), None if dB is None else dB.to(B.dtype), None, None, None,
+                None, None, None, None)
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """x [T, d], weight [d] or None, residual [T, d] or None -> (y, s, yq, ys): s = x + residual (None without one),
+    y the normalized rows, yq and ys their 8-bit rows and scales (None without fmt; not differentiable: the gradient
+    of a product that reads them comes in through y)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps: float, fmt=None):
+        o = q.qlora_rmsnorm_forward(x, weight, residual=residual, eps=eps, fmt=fmt, save_rstd=True)
+        s = x if residual is None else o.s
+        ctx.has_residual = residual is not None
+        ctx.save_for_backward(s, weight, o.rstd)
+        ctx.set_materialize_grads(False)
+        ctx.mark_non_differentiable(*(t for t in (o.yq, o.ys) if t is not None))
+        return o.y, o.s, o.yq, o.ys
+
+    @staticmethod
+    def backward(ctx, dy, ds, _dyq, _dys):
+        s, weight, rstd = ctx.saved_tensors
+        need_dw = weight is not None and ctx.needs_input_grad[1]
+        if dy is None:  # only the sum was used
+            dx, dw = ds, None
+        else:
+            dx, dw = q.qlora_rmsnorm_backward(dy.contiguous(), s, weight, rstd, ds=None if ds is None else ds.contiguous(),
+                                              need_dw=need_dw)
+        return dx, None if dw is None else dw.to(weight.dtype), dx if ctx.has_residual else None, None, None
+
+
 def _deposit_fp32(p: torch.nn.Parameter, g: torch.Tensor):
     """Keep the float32 gradient beside p.grad: summed while p.grad accumulates, restarted when it is None."""
     prev = getattr(p, "grad_fp32", None)
@@ -80,11 +140,37 @@ class _Bf16Module(torch.nn.Module):
 
         return super()._apply(keep_dtype, recurse)
 
+    def _register_base(self, weight: torch.Tensor, base: str, double_quant: bool):
+        """Quantize the frozen weight (base "nf4" or "fp8") into buffers: frozen state, not parameters."""
+        if base not in ("nf4", "fp8"):
+            raise ValueError(f"base must be 'nf4' or 'fp8', got {base!r}")
+        self.base = base
+        if base == "fp8":
+            w = q.qlora_fp8_quantize(weight)
+            self.register_buffer("codes", w.codes, persistent=True)
+            self.register_buffer("scales", w.scales, persistent=True)
+            return
+        # double_quant=False keeps the float32 absmax of every block (4.5 bits per weight)
+        w = q.qlora_quantize(weight, double_quant=double_quant)
+        self.register_buffer("codes", w.codes, persistent=True)
+        self.register_buffer("qscale", w.qscale, persistent=True)
+        self.register_buffer("smax", w.smax, persistent=True)
+
     @property
-    def w(self) -> q.NF4Weight:
+    def w(self):
         """The quantized weight as the library takes it, built from the registered buffers (so it follows
         device moves and load_state_dict)."""
+        if self.base == "fp8":
+            return q.Fp8Weight(self.d_w_out, self.d_in, self.codes, self.scales)
         return q.NF4Weight(self.d_w_out, self.d_in, self.codes, self.qscale, self.smax)
+
+    def _project(self, x2, A, B, alpha, recompute_u, sink, xq, xs):
+        """One call over the base; xq, xs: the 8-bit rows of x2 (8-bit base only)."""
+        if self.base == "fp8":
+            return Fp8LinearFunction.apply(x2, A, B, self.w, alpha, recompute_u, sink, xq, xs)
+        if xq is not None or xs is not None:
+            raise ValueError("8-bit rows are for a base in 8-bit floating point")
+        return QLoRALinearFunction.apply(x2, A, B, self.w, alpha, recompute_u, sink)
 
 
 class QLoRALinear(_Bf16Module):
@@ -96,17 +182,13 @@ class QLoRALinear(_Bf16Module):
     """
 
     def __init__(self, weight: torch.Tensor, r: int = 8, alpha: float = 16.0, freeze_A: bool = False,
-                 generator: torch.Generator | None = None, double_quant: bool = True, recompute_u: bool = False):
+                 generator: torch.Generator | None = None, double_quant: bool = True, recompute_u: bool = False,
+                 base: str = "nf4"):
         super().__init__()
         if weight.dim() != 2:
             raise ValueError("weight must be [d_out, d_in]")
         d_out, d_in = weight.shape
-        # double_quant=False keeps the float32 absmax of every block (4.5 bits per weight)
-        w = q.qlora_quantize(weight.contiguous(), double_quant=double_quant)
-        # the quantized buffers are frozen state, not parameters
-        self.register_buffer("codes", w.codes, persistent=True)
-        self.register_buffer("qscale", w.qscale, persistent=True)
-        self.register_buffer("smax", w.smax, persistent=True)
+        self._register_base(weight.contiguous(), base, double_quant)
         self.d_out, self.d_in, self.r, self.alpha = d_out, d_in, r, float(alpha)
         self.d_w_out = d_out
         self.recompute_u = recompute_u
@@ -123,16 +205,18 @@ class QLoRALinear(_Bf16Module):
         if dB is not None:
             _deposit_fp32(self.B, dB)
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None) -> torch.Tensor:
+        """xq [tokens, d_in], xs: x's 8-bit rows and scales as QLoRARMSNorm gives them (8-bit base; optional)."""
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.d_in).to(torch.bfloat16).contiguous()
-        h = QLoRALinearFunction.apply(x2, self.A, self.B, self.w, self.alpha, self.recompute_u,
-                                      self._sink if self.r > 0 else None)
+        h = self._project(x2, self.A, self.B, self.alpha, self.recompute_u, self._sink if self.r > 0 else None, xq, xs)
         return h.reshape(*lead, self.d_out)
 
     @torch.no_grad()
     def merged_weight(self) -> torch.Tensor:
-        """bf16 [d_out, d_in] = bf16(W_hat + (alpha/r) B A), for export."""
+        """bf16 [d_out, d_in] = bf16(W_hat + (alpha/r) B A), for export (4-bit base)."""
+        if self.base != "nf4":
+            raise ValueError("merged_weight is for the 4-bit base")
         return q.qlora_merge(self.w, self.A, self.B, self.alpha)
 
 
@@ -150,11 +234,11 @@ class QLoRAFusedLinear(_Bf16Module):
 
     The stacked quantization equals quantizing each projection alone whenever each projection's block count is a
     multiple of the 256-block group (true for the usual shapes: d_out_i * d_in / 64 % 256 == 0), and always with
-    absmax-only storage.
+    absmax-only storage; with an 8-bit base, whenever each d_out_i is a multiple of 128.
     """
 
     def __init__(self, weights, r: int = 8, alpha: float = 16.0, adapted=None, double_quant: bool = True,
-                 generator: torch.Generator | None = None):
+                 generator: torch.Generator | None = None, base: str = "nf4"):
         super().__init__()
         weights = [w.contiguous() for w in weights]
         d_in = weights[0].shape[1]
@@ -168,10 +252,7 @@ class QLoRAFusedLinear(_Bf16Module):
         n_ad = sum(self.adapted) if r > 0 else 0
         if n_ad * r > q.MAX_RANK:
             raise ValueError(f"{n_ad} adapters of rank {r} exceed the library's rank limit {q.MAX_RANK}")
-        w = q.qlora_quantize(torch.cat(weights, 0), double_quant=double_quant)
-        self.register_buffer("codes", w.codes, persistent=True)
-        self.register_buffer("qscale", w.qscale, persistent=True)
-        self.register_buffer("smax", w.smax, persistent=True)
+        self._register_base(torch.cat(weights, 0), base, double_quant)
         self.d_w_out = sum(self.d_outs)
         self.A = torch.nn.ParameterList()
         self.B = torch.nn.ParameterList()
@@ -212,12 +293,34 @@ class QLoRAFusedLinear(_Bf16Module):
                 k += 1
             row0 += d_out
 
-    def forward(self, x: torch.Tensor):
-        """Returns one output per projection, [..., d_out_i] each (views of the single call's output)."""
+    def forward(self, x: torch.Tensor, xq: torch.Tensor | None = None, xs: torch.Tensor | None = None):
+        """Returns one output per projection, [..., d_out_i] each (views of the single call's output). xq, xs: x's 8-bit
+        rows and scales as QLoRARMSNorm gives them (8-bit base; optional)."""
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.d_in).to(torch.bfloat16).contiguous()
         A, B = self.stacked_adapter()
         n_ad = len(self.A)
         alpha = self.alpha * n_ad if n_ad else self.alpha  # scale alpha / (n_ad r) = self.alpha / r
-        h = QLoRALinearFunction.apply(x2, A, B, self.w, alpha, False, self._sink if n_ad else None)
+        h = self._project(x2, A, B, alpha, False, self._sink if n_ad else None, xq, xs)
         return tuple(t.reshape(*lead, t.shape[-1]) for t in torch.split(h, self.d_outs, dim=1))
+
+
+class QLoRARMSNorm(torch.nn.Module):
+    """Root-mean-square norm over the last dimension, with the residual's addition before it and 8-bit rows for an
+    8-bit base's projections after it. weight: float32 or bf16 [dim], or None for ones; fmt: the 8-bit format of the
+    rows (torch.float8_e4m3fn or torch.float8_e5m2), or None for none."""
+
+    def __init__(self, dim: int, eps: float = 1e-6, weight: torch.Tensor | None = None, trainable: bool = False, fmt=None):
+        super().__init__()
+        if weight is not None and tuple(weight.shape) != (dim,):
+            raise ValueError(f"weight must have shape {(dim,)}, got {tuple(weight.shape)}")
+        self.dim, self.eps, self.fmt = int(dim), float(eps), fmt
+        self.weight = None if weight is None else torch.nn.Parameter(weight.detach().clone(), requires_grad=trainable)
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
+        """(y, s, yq, ys): y and s = x + residual in x's shape (s is x without a residual), yq [tokens, dim] and ys the
+        8-bit rows and scales (None without fmt)."""
+        x2 = x.reshape(-1, self.dim)
+        r2 = None if residual is None else residual.reshape(-1, self.dim)
+        y, s, yq, ys = RMSNormFunction.apply(x2, self.weight, r2, self.eps, self.fmt)
+        return y.reshape(x.shape), x if s is None else s.reshape(x.shape), yq, ys

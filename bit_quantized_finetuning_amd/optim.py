@@ -1,4 +1,7 @@
-"""Paged AdamW for the adapter parameters (A, B) of the QLoRA layers.
+"""AdamW for the adapter parameters (A, B) of the QLoRA layers: PagedAdamW, one call per parameter with the state in
+host memory, and FlatAdamW, all parameters in a few launches with the moments in 8 or 32 bits on the GPU.
+
+Paged AdamW:
 
 The first page ("QLoRA는 어떻게 65B 모델을 GPU 한 장에 올렸나", section "메모리 회계", paged-optimizer entry)
 moves the adapters' Adam state out to pinned CPU memory and lets the update run beside the backward. Here each
@@ -190,3 +193,79 @@ class PagedAdamW:
             return
         if self._done is not None:
             torch.cuda.current_stream(self.params[0].device).wait_event(self._done)
+
+
+class FlatAdamW:
+    """AdamW (decoupled weight decay) over all parameters at once (qlora_adamw_many): the moments of every parameter side
+    by side in 8 bits (bits=8: m and sqrt(v) in e4m3 with a scale per 256 elements, rounded stochastically by bits that
+    depend on `seed`, the step and the place) or in 32, a float32 master copy of bf16 parameters, and the gradients
+    scaled to a global norm of at most `max_norm` when given. A norm that is not finite leaves the parameters and moments
+    as they were (the step still counts); parameters without a gradient are skipped.
+
+    step() runs on the caller's current stream, from the layers' float32 gradients (`grad_fp32`) when every parameter
+    with a gradient has one, else from autograd's; `norm` is the last step's gradient norm, on the device."""
+
+    def __init__(self, params, lr: float = 1e-4, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+                 bits: int = 8, max_norm: float | None = None, seed: int = 0):
+        self.params = [p for p in params if p.requires_grad]
+        if not self.params:
+            raise ValueError("no trainable parameters")
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits}")
+        dtype, dev = self.params[0].dtype, self.params[0].device
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"parameters must be bfloat16 or float32, got {dtype}")
+        for p in self.params:
+            if p.dtype != dtype or p.device != dev or not p.is_contiguous():
+                raise TypeError("parameters must be contiguous, of one dtype and on one device")
+        self.lr, self.betas, self.eps, self.weight_decay = float(lr), tuple(betas), float(eps), float(weight_decay)
+        self.bits, self.max_norm, self.seed, self.step_count, self.norm = bits, max_norm, int(seed), 0, None
+        n = q.adamw_state_elements([p.numel() for p in self.params])
+        held = q.E4M3 if bits == 8 else torch.float32
+        self.m, self.v = torch.zeros(n, device=dev).to(held), torch.zeros(n, device=dev).to(held)
+        self.m_scale = self.v_scale = None
+        if bits == 8:
+            self.m_scale = torch.zeros(n // q.ADAMW_BLOCK, device=dev)
+            self.v_scale = torch.zeros(n // q.ADAMW_BLOCK, device=dev)
+        self.master = None
+        if dtype == torch.bfloat16:
+            self.master = torch.zeros(n, device=dev)
+            at = 0
+            for p in self.params:
+                self.master[at:at + p.numel()] = p.detach().reshape(-1)
+                at += -(-p.numel() // q.ADAMW_BLOCK) * q.ADAMW_BLOCK
+
+    def zero_grad(self):
+        for p in self.params:
+            p.grad = None
+            p.grad_fp32 = None
+
+    @torch.no_grad()
+    def step(self):
+        self.step_count += 1
+        wide = [getattr(p, "grad_fp32", None) if p.grad is not None else None for p in self.params]
+        if all((w is None) == (p.grad is None) for w, p in zip(wide, self.params)):
+            grads = wide
+        else:
+            grads = [p.grad for p in self.params]
+        grads = [None if g is None else g.detach().contiguous() for g in grads]
+        self.norm = q.qlora_adamw_many(self.step_count, grads, [p.data for p in self.params], self.m, self.v, self.m_scale,
+                                       self.v_scale, master=self.master, lr=self.lr, beta1=self.betas[0],
+                                       beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
+                                       max_norm=self.max_norm, seed=self.seed)
+
+    def state_dict(self) -> dict:
+        return {"step": self.step_count, "bits": self.bits, "m": self.m, "v": self.v, "m_scale": self.m_scale,
+                "v_scale": self.v_scale, "master": self.master}
+
+    def load_state_dict(self, state: dict):
+        if state["bits"] != self.bits:
+            raise ValueError(f"the state holds {state['bits']}-bit moments, this optimizer {self.bits}-bit ones")
+        with torch.no_grad():
+            for k in ("m", "v", "m_scale", "v_scale", "master"):
+                mine, theirs = getattr(self, k), state[k]
+                if (mine is None) != (theirs is None) or (mine is not None and mine.shape != theirs.shape):
+                    raise ValueError(f"{k} does not fit these parameters")
+                if mine is not None:
+                    mine.copy_(theirs)
+        self.step_count = int(state["step"])

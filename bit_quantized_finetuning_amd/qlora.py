@@ -1044,8 +1044,8 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
                      beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
                      max_norm: float | None = None, seed: int = 0, norm: torch.Tensor | None = None,
                      ws: torch.Tensor | None = None) -> torch.Tensor | None:
-    """One AdamW step over lists of gradients (all float32 or all bfloat16) and parameters (all float32, or all
-    bfloat16 with a float32 `master` copy), in place.
+    """One AdamW step over lists of gradients (all float32 or all bfloat16; None leaves that parameter and its moments
+    as they are) and parameters (all float32, or all bfloat16 with a float32 `master` copy), in place.
 
     m, v, master are flat: tensor i's elements start after those of the tensors before it, each rounded up to a
     multiple of 256 (adamw_state_elements of the sizes in all). float32 m and v hold the moments; float8_e4m3fn ones
@@ -1065,7 +1065,8 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     if not torch.is_tensor(m) or not torch.is_tensor(v):
         raise TypeError("m and v must be tensors")
     dev = m.device
-    gd, pd = (grads[0].dtype, params[0].dtype) if count else (torch.float32, torch.float32)
+    gd = next((g.dtype for g in grads if g is not None), torch.float32)
+    pd = params[0].dtype if count else torch.float32
     if gd not in _FLOAT or pd not in _FLOAT:
         raise TypeError(f"gradients and parameters must be float32 or bfloat16, got {gd} and {pd}")
     jobs = (_AdamWJob * max(count, 1))()
@@ -1073,15 +1074,15 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     for i in range(count):
         g, p = grads[i], params[i]
         n = p.numel()
-        if g.dtype is not gd or p.dtype is not pd:
+        if (g is not None and g.dtype is not gd) or p.dtype is not pd:
             raise TypeError(f"tensor {i}: all gradients must be {gd} and all parameters {pd}")
-        if g.numel() != n or not g.is_contiguous() or not p.is_contiguous():
+        if not p.is_contiguous() or (g is not None and (g.numel() != n or not g.is_contiguous())):
             raise ValueError(f"tensor {i}: gradient and parameter must be contiguous and of one size")
-        if g.device != dev or p.device != dev:
-            raise ValueError(f"tensor {i} is on {g.device} / {p.device}, the state on {dev}")
+        if p.device != dev or (g is not None and g.device != dev):
+            raise ValueError(f"tensor {i} is not on {dev}, where the state is")
         j = jobs[i]
         at = p.data_ptr()
-        j.grad, j.param, j.n = g.data_ptr(), at, n
+        j.grad, j.param, j.n = None if g is None else g.data_ptr(), at, n
         total += -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
         if n:
             spans.append((at, at + n * p.element_size()))

@@ -15,6 +15,10 @@ stands in for parts of the model that are not on this path:
 With checkpoint=True each layer keeps only its input and runs its forward again in the backward
 (torch.utils.checkpoint, non-reentrant).
 
+base="fp8" keeps the projections' frozen weights in 8-bit floating point instead: the norms are then the library's
+(QLoRARMSNorm), which write the 8-bit rows that q/k/v and gate/up multiply, and the one before the MLP adds the
+residual in the same pass.
+
 Weights come from the seeded device generator of the synthetic-input module, one seed per layer, so that a
 layer's weights can be drawn again to check it.
 """
@@ -26,7 +30,8 @@ import torch.nn.functional as F
 from torch.utils.checkpoint import checkpoint
 
 from . import synth
-from .layer import QLoRAFusedLinear, QLoRALinear
+from . import qlora as q_
+from .layer import QLoRAFusedLinear, QLoRALinear, QLoRARMSNorm
 
 HEAD = 128
 
@@ -41,29 +46,44 @@ class DecoderProjections(torch.nn.Module):
     bf16 [d_out, d_in] tensors."""
 
     def __init__(self, weights: dict, r: int = 8, alpha: float = 16.0, generator: torch.Generator | None = None,
-                 head: int = HEAD):
+                 head: int = HEAD, base: str = "nf4"):
         super().__init__()
+        self.base = base
         self.hidden, self.kv, self.head = weights["q"].shape[0], weights["k"].shape[0], head
         if self.hidden % head or self.kv % head or self.hidden % self.kv:
             raise ValueError("q and k/v widths must be multiples of the head width, q's of k's")
         self.qkv = QLoRAFusedLinear([weights["q"], weights["k"], weights["v"]], r=r, alpha=alpha,
-                                    adapted=[True, False, True], generator=generator)
-        self.o = QLoRALinear(weights["o"], r=0)
-        self.gate_up = QLoRAFusedLinear([weights["gate"], weights["up"]], r=0)
-        self.down = QLoRALinear(weights["down"], r=0)
+                                    adapted=[True, False, True], generator=generator, base=base)
+        self.o = QLoRALinear(weights["o"], r=0, base=base)
+        self.gate_up = QLoRAFusedLinear([weights["gate"], weights["up"]], r=0, base=base)
+        self.down = QLoRALinear(weights["down"], r=0, base=base)
+        self.norm = QLoRARMSNorm(self.hidden, fmt=q_.E4M3) if base == "fp8" else None
 
     def _heads(self, t: torch.Tensor, rep: int) -> torch.Tensor:
         """[T, n * head] -> [T, kv heads, rep, head] (a view; k and v broadcast over the query heads they serve)."""
         return t.view(t.shape[0], self.kv // self.head, rep, self.head)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if self.base == "fp8":
+            return self._forward_fp8(x)
         q, k, v = self.qkv(rms_norm(x))
-        rep = self.hidden // self.kv  # query heads per KV head
-        # a = q * sigmoid(k) + v with k and v broadcast to the query heads (one bf16 rounding, float32 inside)
-        a = torch.addcmul(self._heads(v, 1), self._heads(q, rep), torch.sigmoid(self._heads(k, 1)))
+        a = self._mix(q, k, v)
         x1 = x + self.o(a.reshape(x.shape[0], self.hidden))
         g, u = self.gate_up(rms_norm(x1))
         return x1 + self.down(F.silu(g) * u)
+
+    def _forward_fp8(self, x: torch.Tensor) -> torch.Tensor:
+        y, _, yq, ys = self.norm(x)
+        q, k, v = self.qkv(y, yq, ys)
+        a = self._mix(q, k, v)
+        y, x1, yq, ys = self.norm(self.o(a.reshape(x.shape[0], self.hidden)), residual=x)
+        g, u = self.gate_up(y, yq, ys)
+        return x1 + self.down(F.silu(g) * u)
+
+    def _mix(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> torch.Tensor:
+        rep = self.hidden // self.kv  # query heads per KV head
+        # a = q * sigmoid(k) + v with k and v broadcast to the query heads (one bf16 rounding, float32 inside)
+        return torch.addcmul(self._heads(v, 1), self._heads(q, rep), torch.sigmoid(self._heads(k, 1)))
 
 
 class DecoderStack(torch.nn.Module):
@@ -71,7 +91,7 @@ class DecoderStack(torch.nn.Module):
     to the 14B-style layer) and its adapters' A are drawn from synth.stack_adapter_init(i) (B starts at zero)."""
 
     def __init__(self, layers: int = 40, shapes: dict | None = None, r: int = 8, alpha: float = 16.0,
-                 seed: int = 0, device="cuda", checkpoint: bool = True, head: int = HEAD):
+                 seed: int = 0, device="cuda", checkpoint: bool = True, head: int = HEAD, base: str = "nf4"):
         super().__init__()
         self.shapes = dict(synth.STACK_SHAPES if shapes is None else shapes)
         self.seed = seed
@@ -80,7 +100,7 @@ class DecoderStack(torch.nn.Module):
         for i in range(layers):
             ws = synth.stack_layer_weights(i, device, self.shapes, seed)
             gen = synth.stack_adapter_init(i, device, seed)
-            self.layers.append(DecoderProjections(ws, r=r, alpha=alpha, generator=gen, head=head))
+            self.layers.append(DecoderProjections(ws, r=r, alpha=alpha, generator=gen, head=head, base=base))
             del ws
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:

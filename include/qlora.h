@@ -398,7 +398,8 @@ size_t qlora_rmsnorm_workspace_bytes(int64_t T, int64_t d);
  * the moments in 32 bits or in 8.
  *   jobs     host array: each tensor's gradient (grad_dtype f32 or bf16),
  *            parameter (param_dtype f32: updated in place; bf16: receives
- *            bf16(master)) and number of elements (0 is allowed)
+ *            bf16(master)) and number of elements (0 is allowed). A tensor whose
+ *            gradient is NULL keeps its place in the state and is left as it is
  *   state    host struct; tensor i's elements begin at off_i = the sum over the
  *            tensors before it of n rounded up to QLORA_ADAMW_BLOCK:
  *              dtype QLORA_F32   m, v f32

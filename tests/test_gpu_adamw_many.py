@@ -248,3 +248,49 @@ def test_captured_step(bits):
         assert torch.equal(want, norm), k
         for x, y in ((a.m, b.m), (a.v, b.v), (a.master, b.master)):
             assert torch.equal(x.float(), y.float()), k
+
+
+@pytest.mark.parametrize("clip", [None, 0.01])
+@pytest.mark.parametrize("missing", [[0], [1, 2], [4], [0, 2, 4], [0, 1, 2, 3, 4]])
+def test_tensors_without_a_gradient_are_left_alone(missing, clip):
+    """The others get what they get in a call of their own (32-bit moments: nothing depends on the place)."""
+    say(f"adamw many without gradients {missing} clip={clip}")
+    sizes = [300, 5000, 256, 0, 777]
+    a = Setup(sizes, 32, torch.float32, torch.bfloat16, "h")
+    before = a.clone()
+    for i in missing:
+        a.grads[i] = None
+    a.step(3, max_norm=clip)
+    b = before.clone()
+    here = [i for i in range(5) if i not in missing]
+    if here:
+        cut = lambda t: torch.cat([t[b.offs[i]:b.offs[i] + R.padded(sizes[i])] for i in here])  # noqa: E731
+        m, v, master = cut(b.m), cut(b.v), cut(b.master)
+        q.qlora_adamw_many(3, [b.grads[i] for i in here], [b.params[i] for i in here], m, v, master=master, max_norm=clip, **HP)
+        assert torch.equal(cut(a.m), m) and torch.equal(cut(a.v), v) and torch.equal(cut(a.master), master)
+    for i in range(5):
+        o = slice(a.offs[i], a.offs[i] + sizes[i])
+        if i in missing:
+            assert torch.equal(a.m[o], before.m[o]) and torch.equal(a.master[o], before.master[o])
+            assert torch.equal(a.params[i], before.params[i])
+        else:
+            assert torch.equal(a.params[i], b.params[i])
+
+
+def test_python_and_native_marshalling_agree(monkeypatch):
+    say("adamw many python marshalling")
+    runs = []
+    for native in (True, False):
+        if not native:
+            monkeypatch.setattr(q, "_marshal", _Refuses())
+        s = Setup(SIZES["edges"], 8, torch.float32, torch.bfloat16, "m")
+        s.grads[4] = None
+        norm = s.step(4, max_norm=0.05, seed=3)
+        runs.append((s.m.view(torch.uint8), s.v.view(torch.uint8), s.ms, s.vs, s.master, norm, *s.params))
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+
+
+class _Refuses:
+    def __getattr__(self, name):
+        return lambda *a: None

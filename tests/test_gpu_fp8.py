@@ -351,3 +351,26 @@ def test_streaming_forward_without_its_producers(T, N, K, r):
         assert torch.equal(h1, h) and torch.equal(u1, u)
     say(f"    partials formed by readers: {q.qlora_workspace_fallbacks(ws)}")
     q.qlora_workspace_set_wait_limit(ws, 0)
+
+
+class _Refuses:
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_python_and_native_marshalling_agree(T, monkeypatch):
+    say(f"fp8 python marshalling T={T}")
+    N, K, r = 272, 400, 16
+    g = _gen("m", T)
+    w, x, dY = _weight(g, N, K), _rows(g, T, K), _rows(g, T, N)
+    A, B = _adapter(g, N, K, r)
+    xq, xs = q.qlora_fp8_quantize_rows(x, R.E5M2)
+    runs = []
+    for native in (True, False):
+        if not native:
+            monkeypatch.setattr(q, "_marshal", _Refuses())
+        runs.append(q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True) + q.qlora_fp8_forward(w, None, None, None, 1.0, xq=xq, xs=xs, fmt=R.E5M2)[:1]
+                    + q.qlora_fp8_backward(w, x, dY, A, B, 16.0))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)

@@ -209,3 +209,22 @@ def test_captured_norm():
         torch.cuda.synchronize()
         for a, b in zip(want, outs):
             assert torch.equal(a.float(), b.float())
+
+
+class _Refuses:
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def test_python_and_native_marshalling_agree(monkeypatch):
+    say("norm python marshalling")
+    g = _gen("m")
+    x, res, w, dy = _x(g, 7, 515, torch.bfloat16, 3, 1), _x(g, 7, 515, torch.bfloat16), _randn(g, 515), _x(g, 7, 515, torch.bfloat16)
+    runs = []
+    for native in (True, False):
+        if not native:
+            monkeypatch.setattr(q, "_marshal", _Refuses())
+        o = q.qlora_rmsnorm_forward(x, w, residual=res, fmt=R.E5M2, save_rstd=True)
+        runs.append(tuple(o) + q.qlora_rmsnorm_backward(dy, o.s, w, o.rstd, ds=dy, need_dw=True))
+    for a, b in zip(*runs):
+        assert torch.equal(a.float(), b.float())

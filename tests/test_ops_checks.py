@@ -135,7 +135,7 @@ def test_adamw_many_refuses():
     assert _many(step=0) == VALUE and _many(max_norm=-1.0) == VALUE and _many(max_norm=float("nan")) == VALUE
     assert _many(jobs=((OK, OK, -1),)) == SHAPE and _many(jobs=((OK, OK, 1 << 38),)) == SHAPE
     assert _many(jobs=((OK, OK, (1 << 38) - 256),) * 3) == SHAPE  # 2^31 blocks and more
-    assert _many(jobs=((None, OK, 1),)) == NULL and _many(jobs=((OK, OK, 5), (OK, None, 1))) == NULL
+    assert _many(jobs=((OK, OK, 5), (OK, None, 1))) == NULL
     assert _many(jobs=((OK, OK, 5), (OFF, OK, 1))) == ALIGN
     assert _many(m=None) == NULL and _many(m=OFF) == ALIGN
     assert _many(sd=E4M3) == NULL and _many(sd=E4M3, ms=OK) == NULL  # scales
@@ -145,6 +145,7 @@ def test_adamw_many_refuses():
     assert _many(max_norm=1.0, norm=OK, ws=OK, n=need - 1) == WORKSPACE
     assert _many(max_norm=1.0, norm=OK, n=need) == NULL
     assert _many(jobs=(), m=None, v=None) == 0 and _many(jobs=((None, None, 0),), m=None, v=None) == 0
+    assert _many(jobs=((None, OK, 5),)) == 0  # no gradient: left as it is
 
 
 # --- the binding -------------------------------------------------------------
