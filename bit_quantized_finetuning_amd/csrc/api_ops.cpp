@@ -53,15 +53,14 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   L.q8 = take((size_t)T * d);
   L.qs = take((size_t)T * groups(d) * 4);
   size_t pf = 0;
-  if (r > 0 && T < kWideMinTokens) {
-    pf = std::max(pf, (size_t)ceil_div(T, 16) * lora_small_ksplit(T, d) * 16 * rp);
-    pf = std::max(pf, lora_grad_partial_floats(r, d_in, T));
-    pf = std::max(pf, lora_grad_partial_floats(d_out, r, T));
-  } else if (r > 0) {
-    pf = std::max(pf, lora_tall_partial_floats(T, d_in, rp));
-    pf = std::max(pf, lora_tall_partial_floats(T, d_out, rp));
-    pf = std::max(pf, lora_wgrad_partial_floats(d_in, r, T));
-    pf = std::max(pf, lora_wgrad_partial_floats(d_out, r, T));
+  if (r > 0) {
+    if (T < kWideMinTokens) {
+      pf = std::max(pf, (size_t)ceil_div(T, 16) * lora_small_ksplit(T, d) * 16 * rp);
+    } else {
+      pf = std::max(pf, lora_tall_partial_floats(T, d_in, rp));
+      pf = std::max(pf, lora_tall_partial_floats(T, d_out, rp));
+    }
+    pf = std::max(pf, adapter_grad_partial_floats(d_in, d_out, r, T));
   }
   pf = std::max(pf, fp8_partial_floats(T, d_out, d_in, false));
   pf = std::max(pf, fp8_partial_floats(T, d_in, d_out, true));
@@ -183,44 +182,22 @@ int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint1
   uint16_t *sv = at<uint16_t>(ws, L.su);
   float *v = at<float>(ws, L.v), *partial = at<float>(ws, L.partial);
   uint32_t *counters = at<uint32_t>(ws, 0), *fallbacks = counters + kMaxCounters - 1;
-  hipError_t e = hipSuccess;
-  if (r > 0 && (dX || dA)) {
-    uint16_t *bt = at<uint16_t>(ws, L.bt);
-    if ((e = launch_transpose_bf16(B, d_out, r, bt, stream)) != hipSuccess) return QLORA_ERR_HIP;
-    if ((e = adapter_product(dY, bt, T, d_out, r, sc, v, sv, partial, counters, stream)) != hipSuccess)
-      return QLORA_ERR_HIP;
+  uint8_t *q = dX ? at<uint8_t>(ws, L.q8) : nullptr;
+  float *qs = at<float>(ws, L.qs);
+  uint16_t *bt = r > 0 && (dX || dA) ? at<uint16_t>(ws, L.bt) : nullptr, *lt = r > 0 && dX ? at<uint16_t>(ws, L.lt) : nullptr;
+  hipError_t e = launch_fp8_prepare_backward(dY, T, d_out, d_in, fmt == QLORA_E5M2, q, qs, A, B, r, lt, bt, stream);
+  if (e == hipSuccess && bt) e = adapter_product(dY, bt, T, d_out, r, sc, v, sv, partial, counters, stream);
+  if (e == hipSuccess && dX)
+    e = launch_fp8_product(W->codes, W->scales, d_out, d_in, true, q, qs, fmt == QLORA_E5M2, T, sv, rank_pad(r), lt, r,
+                           dX, partial, counters, stream);
+  const float *u = u_saved;
+  if (e == hipSuccess && dB && !u) {
+    u = at<float>(ws, L.u);
+    e = adapter_product(x, A, T, d_in, r, 1.f, at<float>(ws, L.u), nullptr, partial, counters, stream);
   }
-  if (dX) {
-    uint8_t *q = at<uint8_t>(ws, L.q8);
-    float *qs = at<float>(ws, L.qs);
-    uint16_t *at_ = at<uint16_t>(ws, L.lt);
-    e = launch_fp8_quantize_rows(dY, true, T, d_out, fmt == QLORA_E5M2, q, qs, stream);
-    if (e == hipSuccess && r > 0) e = launch_transpose_bf16(A, r, d_in, at_, stream);
-    if (e == hipSuccess)
-      e = launch_fp8_product(W->codes, W->scales, d_out, d_in, true, q, qs, fmt == QLORA_E5M2, T, sv, rank_pad(r), at_,
-                             r, dX, partial, counters, stream);
-    if (e != hipSuccess) return QLORA_ERR_HIP;
-  }
-  const bool wide = T >= kWideMinTokens;
-  if (dA) {
-    e = wide ? launch_lora_wgrad(x, v, T, d_in, r, true, sc, dA, partial, counters, fallbacks, stream)
-             : launch_lora_grad(v, true, r, x, false, d_in, T, sc, dA, partial, counters, lora_grad_ksplit(r, d_in, T),
-                                stream);
-    if (e != hipSuccess) return QLORA_ERR_HIP;
-  }
-  if (dB) {
-    const float *u = u_saved;
-    if (!u) {
-      float *uw = at<float>(ws, L.u);
-      if ((e = adapter_product(x, A, T, d_in, r, 1.f, uw, nullptr, partial, counters, stream)) != hipSuccess)
-        return QLORA_ERR_HIP;
-      u = uw;
-    }
-    e = wide ? launch_lora_wgrad(dY, u, T, d_out, r, false, sc, dB, partial, counters, fallbacks, stream)
-             : launch_lora_grad(dY, false, d_out, u, true, r, T, sc, dB, partial, counters,
-                                lora_grad_ksplit(d_out, r, T), stream);
-    if (e != hipSuccess) return QLORA_ERR_HIP;
-  }
+  if (e == hipSuccess)
+    e = launch_adapter_grad({x, v, dA, d_in}, {dY, u, dB, d_out}, T, r, sc, partial, counters, fallbacks, stream);
+  if (e != hipSuccess) return QLORA_ERR_HIP;
   return QLORA_OK;
 }
 

@@ -184,6 +184,26 @@ int lora_grad_ksplit(int64_t M, int64_t N, int64_t T);
 size_t lora_grad_partial_floats(int64_t M, int64_t N, int64_t T);
 int lora_grad_tiles(int64_t M, int64_t N);
 
+// adapter_grad.hip: the adapter gradients of the 8-bit base's backward, X bf16 [T, D], Y float32 [T, R] (R % 8 == 0,
+// D % 16 == 0). a: out[R, D] = scale Y^T X (dA); b: out[D, R] = scale X^T Y (dB); a job with out == NULL is none. Uses
+// `partial` (adapter_grad_partial_floats) and `counters` (one tile_counter per output tile); counts in *fallbacks the
+// waits that ran out of time (the result does not depend on them).
+struct AdapterGradJob {
+  const uint16_t *X;
+  const float *Y;
+  float *out;
+  int64_t D;
+};
+hipError_t launch_adapter_grad(const AdapterGradJob &a, const AdapterGradJob &b, int64_t T, int R, float scale,
+                               float *partial, uint32_t *counters, uint32_t *fallbacks, hipStream_t st);
+size_t adapter_grad_partial_floats(int64_t Da, int64_t Db, int R, int64_t T);
+
+// fp8_quant.hip: what the backward needs before its products, in one launch: the rows of dY [T, d_out] in 8 bits (codes
+// == NULL: not), B^T [r, d_out] (bt == NULL: not) and A^T [d_in, r] (lt == NULL: not).
+hipError_t launch_fp8_prepare_backward(const uint16_t *dY, int64_t T, int64_t d_out, int64_t d_in, bool e5m2,
+                                       uint8_t *codes, float *scales, const uint16_t *A, const uint16_t *B, int r,
+                                       uint16_t *lt, uint16_t *bt, hipStream_t st);
+
 // fp8_quant.hip: rows [T, d] (d % 8 == 0) to 8 bits in groups of 128 with power-of-two scales [T, ceil(d / 128)];
 // a weight [N, K] (K % 8 == 0) to e4m3 in blocks of 128 x 128 with scales [ceil(N / 128), ceil(K / 128)].
 hipError_t launch_fp8_quantize_rows(const void *x, bool bf16_in, int64_t T, int64_t d, bool e5m2, uint8_t *codes,

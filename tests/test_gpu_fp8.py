@@ -175,15 +175,46 @@ def test_backward(T, N, K, r):
         v, vb = D @ Bd, (N + 4) * 2.0 ** -23 * (D.abs() @ Bd.abs())
         ref = ref + s * v @ Ad
         extra = s * ((2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * vb) @ Ad.abs() + (r + 4) * 2.0 ** -23 * v.abs() @ Ad.abs())
-        # dA, dB: a float32 operand enters the matrix units as two bf16 terms (what is left is below 2^-16 of it),
-        # float32 sums over the tokens
-        lim = 2.0 ** -16 + (T + 8) * 2.0 ** -23
+        # dA, dB: a float32 operand enters the matrix units as three bf16 terms (24 bits), float32 sums over the tokens
+        lim = (T + 8) * 2.0 ** -23
         _check("dA", dA, s * v.t() @ X, s * (lim * v.abs().t() + vb.t()) @ X.abs())
         U, ub = X @ Ad.t(), (K + 4) * 2.0 ** -23 * (X.abs() @ Ad.abs().t())
         _check("dB", dB, s * D.t() @ U, s * D.abs().t() @ (lim * U.abs() + ub))
     else:
         assert dA is None and dB is None
     _check("dX", dX, ref, R.product_bound(yh, wh, ref, extra))
+
+
+@pytest.mark.parametrize("T,N,K,r", [(1, 16, 272, 8), (2, 528, 16, 16), (5, 1040, 784, 24), (33, 256, 512, 64),
+                                     (40, 272, 144, 72), (64, 144, 1040, 128), (65, 784, 400, 136), (97, 512, 256, 256)])
+def test_adapter_gradients_keep_float32(T, N, K, r):
+    """The intermediates enter with all their bits. u is given, in float32. v = dY B has 24 bits by construction: each
+    column of B holds 1, 2^-8 and 2^-16 at three rows, and each sum over dY's values there is exact in float32."""
+    say(f"fp8 adapter gradients T={T} {N}x{K} r={r}")
+    g = _gen(T, N, K, r, "keep")
+    w = _weight(g, N, K)
+    x, u = _rows(g, T, K), _randn(g, T, r)
+    dY = ((128 + torch.randint(0, 128, (T, N), generator=g, device="cuda")) / 256.0).bfloat16()  # 1/2 .. 1, 8 bits
+    B = torch.zeros(N, r, device="cuda")
+    for j in range(r):
+        for i, at in enumerate(torch.randperm(N, generator=g, device="cuda")[:3].tolist()):
+            B[at, j] = 2.0 ** (-8 * i)
+    A, B = _adapter(g, N, K, r)[0], B.bfloat16()
+    v = dY.double() @ B.double()
+    assert torch.equal(v.float().double(), v)
+    s = 32.0 / r
+    # three terms leave at most 2^-25 of a value behind; T sums, the scale and its product, one step each
+    lim = s * (T + 4) * 2.0 ** -23
+    for want in ("both", "dA", "dB"):
+        _, dA, dB = q.qlora_fp8_backward(w, x, dY, A, B, 32.0, u_saved=u, need_dx=False, need_dA=want != "dB", need_dB=want != "dA")
+        if want != "dB":
+            _check(f"dA ({want})", dA, s * v.t() @ x.double(), lim * v.abs().t() @ x.double().abs())
+        else:
+            assert dA is None
+        if want != "dA":
+            _check(f"dB ({want})", dB, s * dY.double().t() @ u.double(), lim * dY.double().abs().t() @ u.double().abs())
+        else:
+            assert dB is None
 
 
 @pytest.mark.parametrize("fmt", FMTS)
