@@ -11,7 +11,7 @@
 // than all the rest of the sum does; the third product costs nothing here, as
 // the matrix unit waits for X.)
 //
-// A workgroup owns 256 columns of X (64 per wave), up to 128 ranks and a range
+// A workgroup owns 256 columns of X (64 per wave), up to 64 ranks and a range
 // of tokens, in steps of 32 tokens. X tiles are copied into LDS two steps ahead
 // and Y tiles one step ahead; each lane converts the 16 bytes of Y that it
 // copied itself, so one barrier a step is enough. Both operands need 8
@@ -21,6 +21,9 @@
 //
 // Token ranges of a tile store float32 tiles and share their sum, in range
 // order (split_arrive in common.h): the result does not depend on who sums it.
+// Measured: 4096 tokens, 22016 + 8192 columns, rank 64: 60 us, 4.1 TB/s of X;
+// 333 tokens, 5120 + 5120 columns, rank 16: 8.1 us, most of it the launch, three
+// steps' latency and the sum.
 #include <type_traits>
 
 #include "kernels.h"
@@ -32,7 +35,7 @@ constexpr int kAgD = 256, kAgTok = 32;
 constexpr int kAgX = kAgTok * 2 * kAgD;  // bytes of an X tile
 constexpr int kAgMaxSplit = 16;
 
-template <int NR>  // tiles of 16 ranks per workgroup
+template <int NR>  // tiles of 16 ranks per workgroup: 1, 2 or 4
 struct AgSize {
   static constexpr int raw = NR == 1 ? 4096 : 2048 * NR;   // float32 Y as copied: 1 KB a copy, every wave the same copies
   static constexpr int plane = 1024 * NR;                  // one bf16 term of a Y tile
@@ -54,7 +57,7 @@ __device__ __forceinline__ int yturn(int n) {
 }
 
 template <int NR>
-__global__ __launch_bounds__(256, NR <= 4 ? 2 : 1) void k_adapter_grad(
+__global__ __launch_bounds__(256, 2) void k_adapter_grad(
     AdapterGradJob ja, AdapterGradJob jb, int tiles_a, int64_t T, int R, float scale, float *__restrict__ partial,
     uint32_t *__restrict__ counters, uint32_t *__restrict__ fallbacks, int ksplit) {
   using S = AgSize<NR>;
@@ -269,22 +272,34 @@ __global__ __launch_bounds__(256, NR <= 4 ? 2 : 1) void k_adapter_grad(
 }
 
 namespace {
-int ag_tiles16(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+// Ranks above 64 are cut into chunks of 64 that read X again: two workgroups per CU hide each other's waits, which a
+// chunk of 128 (112 KB of LDS) does not allow (4096 tokens, 22016 + 8192 columns, rank 128: 104 us against 130).
+int ag_tiles16(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : 4; }
 int64_t ag_tiles(int64_t D, int R) {
   const int rt = 16 * ag_tiles16(R);
   return ((D + kAgD - 1) / kAgD) * ((R + rt - 1) / rt);
 }
-// Ranges: as many as keep every workgroup of the launch resident (two per CU with up to 64 ranks, one above), since
-// the ranges of a tile wait for each other; at least one step each.
+// Ranges of tokens, a power of two, by estimated time in ns: a workgroup's steps (or X's bytes, if memory takes longer),
+// and for a split what its tiles' stores and sums add. All workgroups fit on the card at two per CU, since the ranges of
+// a tile wait for each other. Ranges 1 / 2 / 4 / 8 measured: 333 tokens, 5120 + 5120 columns, rank 16: 8.6 / 9.2 / 8.1 /
+// 12.3 us, rank 128: 15.7 / 15.9 / 19.4 / 29 us; 4096 tokens, 22016 + 8192 columns, rank 64: 128 / 75 / 60 / 79 us.
 int ag_ksplit(int64_t tiles, int R, int64_t T) {
-  const int64_t room = (int64_t)device_cu_count(current_device()) * (R <= 64 ? 2 : 1), nkt = (T + kAgTok - 1) / kAgTok;
+  const int64_t room = 2 * (int64_t)device_cu_count(current_device()), nkt = (T + kAgTok - 1) / kAgTok;
+  const int nr = ag_tiles16(R);
   if (tiles > kMaxTileCounters) return 1;
-  int64_t ks = room / tiles;
-  if (ks > nkt) ks = nkt;
-  if (ks > kAgMaxSplit) ks = kAgMaxSplit;
-  if (ks < 1) ks = 1;
-  while (ks & (ks - 1)) ks &= ks - 1;
-  return (int)ks;
+  const double step = 450. + 140. * nr, memory = (double)tiles * kAgD * 2 * (double)T / 4400.;
+  double best = 0;
+  int pick = 1;
+  for (int ks = 1; ks <= kAgMaxSplit && ks <= nkt && (ks == 1 || tiles * ks <= room); ks *= 2) {
+    const double steps = step * (double)((nkt + ks - 1) / ks);
+    double t = steps > memory ? steps : memory;
+    if (ks > 1) t += 2500. + 0.4e-3 * (double)(tiles * ks) * 16 * nr * kAgD * 4;
+    if (ks == 1 || t < best) {
+      best = t;
+      pick = ks;
+    }
+  }
+  return pick;
 }
 
 template <int NR>
@@ -321,8 +336,7 @@ hipError_t launch_adapter_grad(const AdapterGradJob &a, const AdapterGradJob &b,
   switch (ag_tiles16(R)) {
     case 1: return launch_ag<1>(a, b, T, R, scale, partial, counters, fallbacks, st);
     case 2: return launch_ag<2>(a, b, T, R, scale, partial, counters, fallbacks, st);
-    case 4: return launch_ag<4>(a, b, T, R, scale, partial, counters, fallbacks, st);
-    default: return launch_ag<8>(a, b, T, R, scale, partial, counters, fallbacks, st);
+    default: return launch_ag<4>(a, b, T, R, scale, partial, counters, fallbacks, st);
   }
 }
 
