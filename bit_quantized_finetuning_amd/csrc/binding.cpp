@@ -274,10 +274,11 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const float max_norm = (float)as_float(a[13]);
   const int64_t seed = as_int(a[14]);
   const int dev = (int)as_int(a[16]);
-  need(m.defined() && v.defined() && seed >= 0 && seed < ((int64_t)1 << 32) && max_norm >= 0.f);
+  need(m.defined() && v.defined() && seed >= 0 && seed < ((int64_t)1 << 32));
+  need(max_norm > 0.f || as_float(a[13]) == 0.0);  // (0: no clipping; what float32 turns into 0 is refused)
   std::vector<qlora_adamw_job> jobs((size_t)count);
   std::vector<std::pair<uintptr_t, uintptr_t>> spans;
-  spans.reserve((size_t)count);
+  spans.reserve((size_t)count + 6);
   int gd = -1, pd = -1;
   int64_t total = 0;
   for (Py_ssize_t i = 0; i < count; ++i) {
@@ -302,6 +303,11 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     total += (size + QLORA_ADAMW_BLOCK - 1) / QLORA_ADAMW_BLOCK * QLORA_ADAMW_BLOCK;
   }
+  for (const Tensor *t : std::initializer_list<const Tensor *>{&m, &v, &ms, &vs, &master, &norm})
+    if (t->defined() && t->numel()) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(t->data_ptr());
+      spans.emplace_back(at, at + (uintptr_t)t->numel() * t->element_size());
+    }
   std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i) need(spans[i - 1].second <= spans[i].first);
   if (gd < 0) gd = QLORA_F32;

@@ -545,8 +545,9 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 //
 // The adapter's u = x A^T [T, r] is formed by the first workgroups of the same
 // launch (one per 16 ranks and slice of K; the last of the slices to arrive adds
-// them in order) while the others stream, and reaches them as pairs of
-// bf16(s u) that carry the launch's tag. A reader whose wait runs out (other
+// them in order) while the others stream, and reaches them as 64-bit words of
+// one bf16(s u) each with 16 fixed bits that no finite float32 or bf16 an
+// earlier call left in the workspace can hold there, and the launch's tag. A reader whose wait runs out (other
 // launches hold the compute units) forms what it misses itself, in the same
 // order of operations, so no wait needs another workgroup to run and the result
 // does not depend on who formed what. One compute unit reads about 28 GB/s from
@@ -563,10 +564,15 @@ struct StreamAdapter {
   int r, rp, slices;
   float scale;
   float *u_out;
-  uint64_t *ex;    // [16][rp / 2] tagged pairs
+  uint64_t *ex;    // [16][rp] tagged values
   float *partial;  // [rp / 16][slices][4][64] quarters
   uint32_t *counters;
 };
+
+// A value in the exchange: bf16 bits, a pattern that is NaN as the upper half of a float32 and as a bf16, the launch.
+__device__ __forceinline__ uint64_t tagged(uint32_t bits, uint32_t tag) {
+  return (uint64_t)tag << 32 | 0xffa50000u | (bits & 0xffffu);
+}
 
 // Slice ks of K of u for ranks 16 rt .. +15, all tokens: lane l of wave 0 gets token l & 15, ranks 16 rt + 4 (l >> 4) + i.
 __device__ __forceinline__ f32x4 u_partial(const StreamAdapter &a, int K, int T, int rt, int ks, f32x4 (*red)[64]) {
@@ -637,9 +643,9 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
     }
     if (li < T) {
       const int j = 16 * rt + 4 * g;
-      uint64_t *to = ad.ex + (li * ad.rp + j) / 2;
-      st_dev_u64(to, ((uint64_t)pack_bf16x2(u[0] * ad.scale, u[1] * ad.scale) << 32) | tag);
-      st_dev_u64(to + 1, ((uint64_t)pack_bf16x2(u[2] * ad.scale, u[3] * ad.scale) << 32) | tag);
+      uint64_t *to = ad.ex + li * ad.rp + j;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st_dev_u64(to + i, tagged(pack_bf16x2(u[i] * ad.scale, 0.f), tag));
       if (ad.u_out && j < ad.r) *reinterpret_cast<f32x4 *>(ad.u_out + li * ad.r + j) = u;
     }
     return;
@@ -681,20 +687,30 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
     }
   }
   if (producers) {
-    const int tiles = ad.rp / 16, pairs = T * ad.rp / 2;
+    constexpr int kAll = 64 * kStreamWaves, kPoll = 4;  // words of a thread asked for at once
+    const int tiles = ad.rp / 16, words = T * ad.rp;
     if (tid < tiles) missing[tid] = 0u;
     __syncthreads();
     const long long t0 = wall_clock64(), limit = wait_limit(ad.counters + kMaxCounters - 1);
-    for (int e = tid; e < pairs; e += 64 * kStreamWaves) {
-      const int t = e / (ad.rp / 2), j = 2 * (e - t * (ad.rp / 2));
+    for (int e0 = tid; e0 < words; e0 += kAll * kPoll) {
       for (;;) {
-        const uint64_t v = ld_dev_u64(ad.ex + e);
-        if ((uint32_t)v == tag) {
-          *reinterpret_cast<uint32_t *>(su + t * kSuPitch + j) = (uint32_t)(v >> 32);
-          break;
-        }
-        if (wall_clock64() - t0 > limit) {
-          missing[j / 16] = 1u;
+        uint64_t v[kPoll];
+        bool all = true;
+#pragma unroll
+        for (int u = 0; u < kPoll; ++u) v[u] = e0 + u * kAll < words ? ld_dev_u64(ad.ex + e0 + u * kAll) : tagged(0u, tag);
+#pragma unroll
+        for (int u = 0; u < kPoll; ++u) all = all && (v[u] >> 16) == (tagged(0u, tag) >> 16);
+        const bool late = !all && wall_clock64() - t0 > limit;
+        if (all || late) {
+#pragma unroll
+          for (int u = 0; u < kPoll; ++u) {
+            const int e = e0 + u * kAll, t = e / ad.rp, j = e - t * ad.rp;
+            if (e >= words) continue;
+            if ((v[u] >> 16) == (tagged(0u, tag) >> 16))
+              su[t * kSuPitch + j] = (uint16_t)v[u];
+            else
+              missing[j / 16] = 1u;
+          }
           break;
         }
         __builtin_amdgcn_s_sleep(1);
@@ -820,8 +836,8 @@ size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? kTileN * 64 * p.mj : kSmN * kSmT);
 }
 
-// the tagged pairs, then the slices' partials
-size_t fp8_stream_exchange_bytes(int rp) { return (size_t)16 * rp / 2 * 8 + (size_t)rp / 16 * kUSlices * 256 * 4; }
+// the tagged values, then the slices' partials
+size_t fp8_stream_exchange_bytes(int rp) { return (size_t)16 * rp * 8 + (size_t)rp / 16 * kUSlices * 256 * 4; }
 
 hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64_t K, const uint8_t *xq, const float *xs,
                              bool e5m2, int64_t T, const uint16_t *x, const uint16_t *A, const uint16_t *B, int r, int rp,
@@ -829,7 +845,7 @@ hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64
                              hipStream_t st) {
   const int slices = (int)std::min<int64_t>(kUSlices, (K + 1023) / 1024);
   const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, static_cast<uint64_t *>(ex),
-                         reinterpret_cast<float *>(static_cast<uint8_t *>(ex) + (size_t)16 * rp / 2 * 8), counters};
+                         reinterpret_cast<float *>(static_cast<uint8_t *>(ex) + (size_t)16 * rp * 8), counters};
   const int producers = r > 0 ? rp / 16 * slices : 0;
   const dim3 grid((unsigned)(N / 16 + producers)), block(64 * kStreamWaves);
   if (e5m2)

@@ -24,6 +24,10 @@ gradient (the adapter's products stay in bf16). The input's 8-bit rows come from
 (QLoRARMSNorm writes them beside its bf16 rows) or are formed within the call; gradients pass straight through that
 rounding.
 
+A training step of these modules can be captured into a graph once nothing keeps an earlier eager step's outputs or
+loss: torch ties a leaf's gradient accumulation to the stream of the graph that lives, and a backward that is captured
+on another stream while an eager one lives ends the process.
+
 The modules compute in bf16 only: a dtype cast of a module (`.to(dtype)`,
 `.half()`, `.float()`) leaves its quantized buffers and adapter parameters as
 they are, and only a device move applies to them. With a frozen A (LoRA-FA: "8GB, 12GB, 16GB, 24GB GPU에서 몇 B

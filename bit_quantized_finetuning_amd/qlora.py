@@ -1034,6 +1034,11 @@ def qlora_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
 # AdamW over many tensors
 # ---------------------------------------------------------------------------
 
+def _neighbours(spans):
+    spans.sort()
+    return zip(spans, spans[1:])
+
+
 def adamw_state_elements(sizes) -> int:
     """Elements of the flat state of tensors of these sizes: each starts at a multiple of 256."""
     return sum(-(-n // ADAMW_BLOCK) * ADAMW_BLOCK for n in sizes)
@@ -1086,8 +1091,7 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
         total += -(-n // ADAMW_BLOCK) * ADAMW_BLOCK
         if n:
             spans.append((at, at + n * p.element_size()))
-    spans.sort()
-    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+    if any(a[1] > b[0] for a, b in _neighbours(spans)):
         raise ValueError("parameters overlap (is one listed twice?)")
     bits8 = m.dtype == E4M3
     if not bits8 and m.dtype != torch.float32:
@@ -1104,10 +1108,15 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     if not 0 <= int(seed) < 1 << 32:
         raise ValueError("seed must fit in 32 bits")
     _arg(norm, "norm", torch.float32, (1,))
+    for t in (m, v, m_scale, v_scale, master, norm):
+        if t is not None and t.numel():
+            spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+    if any(a[1] > b[0] for a, b in _neighbours(spans)):
+        raise ValueError("the state, the parameters and norm must not overlap")
     if max_norm is None and norm is not None:
         raise ValueError("norm is given but max_norm is not")
-    if max_norm is not None and not max_norm > 0:
-        raise ValueError(f"max_norm must be positive, got {max_norm}")
+    if max_norm is not None and not ctypes.c_float(max_norm).value > 0:
+        raise ValueError(f"max_norm must be positive in float32, got {max_norm}")
     _check_devices(dev, v=v, m_scale=m_scale, v_scale=v_scale, master=master, norm=norm, ws=ws)
     hp = _AdamWManyHparams(lr, beta1, beta2, eps, weight_decay)
     st = _AdamWState(2 if bits8 else 0, m.data_ptr(), v.data_ptr(), _ptr(m_scale), _ptr(v_scale), _ptr(master))

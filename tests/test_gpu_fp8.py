@@ -405,3 +405,64 @@ def test_python_and_native_marshalling_agree(T, monkeypatch):
                     + q.qlora_fp8_backward(w, x, dY, A, B, 16.0))
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def _some_rows(T):
+    return torch.tensor(sorted({0, 1, T // 3, T // 2 + 1, T - 130, T - 2, T - 1}), device="cuda")
+
+
+def test_forward_past_32_bit_offsets():
+    """Rows whose 8-bit values, and outputs whose bytes, lie past 2^31 of their tensor's start."""
+    for T, N, K in ((140003, 144, 16400), (70001, 16400, 144)):
+        say(f"fp8 forward T={T} {N}x{K}")
+        g = _gen(T, N)
+        w = _weight(g, N, K)
+        x = torch.randn(T, K, generator=g, device="cuda", dtype=torch.bfloat16)
+        A, B = _adapter(g, N, K, 8)
+        h, u = q.qlora_fp8_forward(w, x, A, B, 8.0, save_u=True)
+        at = _some_rows(T)
+        codes, scales = R.quantize_rows(x[at], R.E4M3)
+        xh, wh, Ad, Bd, X = codes * R.spread_cols(scales, K), R.restored_weight(w.codes, w.scales), A.double(), B.double(), x[at].double()
+        uref, ubound = X @ Ad.t(), (K + 4) * 2.0 ** -23 * (X.abs() @ Ad.abs().t())
+        _check("u", u[at], uref, ubound)
+        ref = xh @ wh.t() + uref @ Bd.t()
+        extra = (2.0 ** -8 * uref.abs() + (1 + 2.0 ** -8) * ubound) @ Bd.abs().t() + 12 * 2.0 ** -23 * uref.abs() @ Bd.abs().t()
+        _check("h", h[at], ref, R.product_bound(xh, wh, ref, extra))
+
+
+def test_backward_past_32_bit_offsets():
+    T, N, K = 140003, 16400, 144
+    say(f"fp8 backward T={T} {N}x{K}")
+    g = _gen(T, N, "b")
+    w = _weight(g, N, K)
+    x = torch.randn(T, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    dY = torch.randn(T, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    A, B = _adapter(g, N, K, 8)
+    u = _randn(g, T, 8)
+    dX, dA, dB = q.qlora_fp8_backward(w, x, dY, A, B, 8.0, u_saved=u)
+    at = _some_rows(T)
+    codes, scales = R.quantize_rows(dY[at], R.E4M3)
+    yh, wh, Ad, Bd, D = codes * R.spread_cols(scales, N), R.restored_weight(w.codes, w.scales).t(), A.double(), B.double(), dY[at].double()
+    v, vb = D @ Bd, (N + 4) * 2.0 ** -23 * (D.abs() @ Bd.abs())
+    ref = yh @ wh.t() + v @ Ad
+    extra = (2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * vb) @ Ad.abs() + 12 * 2.0 ** -23 * v.abs() @ Ad.abs()
+    _check("dX", dX[at], ref, R.product_bound(yh, wh, ref, extra))
+    # The gradients sum over all tokens. A sum of n float32 values in any order is off by at most n steps; the last 300
+    # tokens alone, in a call of their own, show that rows past the offset are the ones that are read.
+    lim = (T + 8) * 2.0 ** -23
+    cols = torch.tensor([0, 5, N // 2, N - 1], device="cuda")
+    Dc, U = dY[:, cols].double(), u.double()
+    _check("dB", dB[cols], Dc.t() @ U, Dc.abs().t() @ (lim * U.abs()))
+    V, Vb, Xd = torch.zeros(T, 8, device="cuda", dtype=torch.float64), torch.zeros(T, 8, device="cuda", dtype=torch.float64), x.double()
+    for i in range(0, T, 20000):
+        d = dY[i:i + 20000].double()
+        V[i:i + 20000], Vb[i:i + 20000] = d @ Bd, d.abs() @ Bd.abs()
+    _check("dA", dA, V.t() @ Xd, (lim * V.abs() + (N + 4) * 2.0 ** -23 * Vb).t() @ Xd.abs())
+    x[:-300] = 0
+    dY[:-300] = 0
+    _, dA, dB = q.qlora_fp8_backward(w, x, dY, A, B, 8.0, u_saved=u, need_dx=False)
+    _, da, db = q.qlora_fp8_backward(w, x[-300:].contiguous(), dY[-300:].contiguous(), A, B, 8.0, u_saved=u[-300:].contiguous(),
+                                     need_dx=False)
+    V, Xd, Dd, U, lim = V[-300:], x[-300:].double(), dY[-300:].double(), u[-300:].double(), 2 * 308 * 2.0 ** -23
+    _check("dA of the last", dA, da.double(), (lim * V.abs() + 2 * (N + 4) * 2.0 ** -23 * Vb[-300:]).t() @ Xd.abs())
+    _check("dB of the last", dB, db.double(), lim * Dd.abs().t() @ U.abs())

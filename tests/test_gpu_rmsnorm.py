@@ -228,3 +228,32 @@ def test_python_and_native_marshalling_agree(monkeypatch):
         runs.append(tuple(o) + q.qlora_rmsnorm_backward(dy, o.s, w, o.rstd, ds=dy, need_dw=True))
     for a, b in zip(*runs):
         assert torch.equal(a.float(), b.float())
+
+
+def test_many_rows_and_far_apart():
+    """More rows than one launch takes, rows past 2^31 bytes, and a row stride of 2^22 elements."""
+    T, d = (1 << 20) + 3, 1032
+    say(f"norm {T}x{d}")
+    g = _gen("many")
+    x, res = (torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    w = 1 + 0.3 * _randn(g, d)
+    o = q.qlora_rmsnorm_forward(x, w, residual=res, fmt=R.E4M3, save_rstd=True)
+    dx, _ = q.qlora_rmsnorm_backward(x, o.s, w, o.rstd, ds=res)
+    dx2, dw = q.qlora_rmsnorm_backward(x, o.s, w, o.rstd, ds=res, need_dw=True)
+    assert torch.equal(dx, dx2)
+    at = torch.tensor([0, 1, T // 2, T - 5, T - 4, T - 3, T - 2, T - 1], device="cuda")
+    some = q.RMSNormOut(*(t[at] for t in o))
+    _check_forward(some, x[at], w, res[at], 1e-6, R.E4M3, torch.bfloat16)
+    ref, mag, _, _ = _ref_backward(x[at], some.s, w, some.rstd, res[at])
+    _within("dx", dx[at], ref, (R.HALF[torch.bfloat16] + 4 * SUM) * mag)
+    total = torch.zeros(2, d, dtype=torch.float64, device="cuda")
+    for i in range(0, T, 1 << 17):
+        p = x[i:i + (1 << 17)].double() * (o.s[i:i + (1 << 17)].double() * o.rstd[i:i + (1 << 17), None].double())
+        total += torch.stack([p.sum(0), p.abs().sum(0)])
+    _within("dw", dw, total[0], (T + 8) * 2.0 ** -23 * total[1])
+    del x, res, o, dx, dx2
+    far = torch.empty(600 << 22, dtype=torch.bfloat16, device="cuda").view(600, 1 << 22)[:, :520]
+    far.copy_(_randn(g, 600, 520))
+    a = q.qlora_rmsnorm_forward(far, None, save_rstd=True)
+    b = q.qlora_rmsnorm_forward(far.contiguous(), None, save_rstd=True)
+    assert torch.equal(a.y, b.y) and torch.equal(a.rstd, b.rstd)

@@ -239,10 +239,16 @@ def test_binding_refuses_adamw_many():
             (lambda: q.qlora_adamw_many(1, [g], [p.bfloat16()], m, v), ValueError),
             (lambda: q.qlora_adamw_many(1, [g], [p], m, v, max_norm=0.0), ValueError),
             (lambda: q.qlora_adamw_many(1, [g], [p], m, v, max_norm=float("nan")), ValueError),
+            (lambda: q.qlora_adamw_many(1, [g], [p], m, v, max_norm=1e-60), ValueError),  # nothing in float32
             (lambda: q.qlora_adamw_many(1, [g], [p], m, v, norm=torch.zeros(1)), ValueError),
             (lambda: q.qlora_adamw_many(1, [g], [p], m, v, seed=-1), ValueError)):
         with pytest.raises(err):
             call()
     with pytest.raises(ValueError, match="overlap"):  # one parameter twice
         q.qlora_adamw_many(1, [g, g], [p, p], torch.zeros(1024), torch.zeros(1024))
+    for call in (lambda: q.qlora_adamw_many(1, [g], [p], m, m),  # one buffer for two things
+                 lambda: q.qlora_adamw_many(1, [g], [m[:300]], m, v),
+                 lambda: q.qlora_adamw_many(1, [g], [p], m, v, max_norm=1.0, norm=v[511:])):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
     assert q.adamw_state_elements([0, 1, 256, 257]) == 256 + 256 + 512
