@@ -294,3 +294,44 @@ def test_python_and_native_marshalling_agree(monkeypatch):
 class _Refuses:
     def __getattr__(self, name):
         return lambda *a: None
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_past_32_bit_places(bits):
+    """A tensor of more than 2^31 elements and one after it: their last elements as in a call on those alone. (8-bit
+    moments round by their place, so their own bits are compared in steps of the format: at most one apart.)"""
+    say(f"adamw {bits}-bit past 32 bits")
+    n, tail = (1 << 31) + 300, 256 + 300
+    total = q.adamw_state_elements([n, 1000])
+    g = _gen("huge", bits)
+    grads = [torch.randn(n, generator=g, device="cuda", dtype=torch.bfloat16), _randn16(g, 1000)]
+    params = [torch.randn(n, generator=g, device="cuda"), torch.randn(1000, generator=g, device="cuda")]
+    cut = n - tail
+    small = q.adamw_state_elements([tail, 1000])
+    few_p, few_g = [params[0][cut:].clone(), params[1].clone()], [grads[0][cut:].clone(), grads[1]]
+    if bits == 32:
+        state = [torch.rand(total, generator=g, device="cuda") for _ in range(2)]
+        few = [t[cut:].clone() for t in state]
+        scales, few_scales = [None, None], [None, None]
+    else:
+        state = [torch.randint(0, 120, (total,), generator=g, device="cuda", dtype=torch.uint8).view(R.E4M3) for _ in range(2)]
+        scales = [torch.rand(total // 256, generator=g, device="cuda") * 1e-4 for _ in range(2)]
+        few = [t[cut:].clone() for t in state]
+        few_scales = [t[cut // 256:].clone() for t in scales]
+    assert few[0].numel() == small
+    q.qlora_adamw_many(3, grads, params, *state, *scales, **HP)
+    q.qlora_adamw_many(3, few_g, few_p, *few, *few_scales, **HP)
+    assert torch.equal(params[0][cut:], few_p[0]) and torch.equal(params[1], few_p[1])
+    for a, b, sa, sb in zip(state, few, scales, few_scales):
+        a = a[cut:]
+        if bits == 32:
+            assert torch.equal(a, b)
+            continue
+        assert torch.equal(sa[cut // 256:], sb)
+        # the codes of e4m3 of one sign are in order: neighbours differ by one (a zero's sign aside)
+        x, y = (torch.where(t >= 128, -(t.int() & 127), t.int()) for t in (a.view(torch.uint8), b.view(torch.uint8)))
+        assert ((x - y).abs() <= 1).all()
+
+
+def _randn16(g, n):
+    return torch.randn(n, generator=g, device="cuda", dtype=torch.bfloat16)

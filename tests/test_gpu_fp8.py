@@ -384,6 +384,23 @@ def test_streaming_forward_without_its_producers(T, N, K, r):
     q.qlora_workspace_set_wait_limit(ws, 0)
 
 
+@pytest.mark.parametrize("T,N,K,r", [(200, 512, 512, 8), (333, 1024, 272, 64), (64, 528, 400, 136)])
+def test_adapter_gradients_without_waiting(T, N, K, r):
+    """With the waits cut to one tick, the last range to arrive adds what the others left: the same bits."""
+    say(f"fp8 adapter gradients, no waits T={T} {N}x{K} r={r}")
+    g = _gen("no waits", T)
+    w, x, dY = _weight(g, N, K), _rows(g, T, K), _rows(g, T, N)
+    A, B = _adapter(g, N, K, r)
+    ws = torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, r), dtype=torch.uint8, device="cuda")
+    want = q.qlora_fp8_backward(w, x, dY, A, B, 16.0, ws=ws)
+    q.qlora_workspace_set_wait_limit(ws, 1)
+    for _ in range(3):
+        for a, b in zip(want, q.qlora_fp8_backward(w, x, dY, A, B, 16.0, ws=ws)):
+            assert torch.equal(a, b)
+    say(f"    waits that ended early: {q.qlora_workspace_fallbacks(ws)}")
+    q.qlora_workspace_set_wait_limit(ws, 0)
+
+
 class _Refuses:
     def __getattr__(self, name):
         return lambda *a: None
