@@ -550,7 +550,10 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 // earlier call left in the workspace can hold there, and the launch's tag. A reader whose wait runs out (other
 // launches hold the compute units) forms what it misses itself, in the same
 // order of operations, so no wait needs another workgroup to run and the result
-// does not depend on who formed what. One compute unit reads about 28 GB/s from
+// does not depend on who formed what. Where the slices' partials are at most one
+// per thread of a reader (one token up to rank 64 of 4096 x 8192, four up to 16),
+// every reader takes and adds those instead, which spares the hop through the
+// last slice (1 token, 4096 x 4096: rank 16 8.6 -> 7.4 us, rank 64 9.3 -> 8.3). One compute unit reads about 28 GB/s from
 // memory, so a slice is kept to about 1024 of K (16 tokens, 4096 x 11008, r =
 // 64: 33.8 us with the whole of K in one workgroup, 19.8 with four slices,
 // 17.0 with eleven).
@@ -558,13 +561,15 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 constexpr int kStreamWaves = 8, kAhead = 4;
 constexpr int kUSlices = 16;  // at most
 constexpr int kSuPitch = QLORA_MAX_RANK + 8;
+constexpr int kDirect = 64 * kStreamWaves;  // partials that a reader takes at most: one per thread
 
 struct StreamAdapter {
   const uint16_t *x, *A, *B;
   int r, rp, slices;
   float scale;
   float *u_out;
-  uint64_t *ex;    // [16][rp] tagged values
+  bool direct;     // readers add the slices' partials themselves
+  uint64_t *ex;    // [T][rp] tagged values; direct: [slices][T][rp][2] tagged halves of float32 partials
   float *partial;  // [rp / 16][slices][4][64] quarters
   uint32_t *counters;
 };
@@ -621,6 +626,18 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
     const int rt = blockIdx.x / ad.slices, ks = blockIdx.x - rt * ad.slices;
     f32x4 u = u_partial(ad, K, T, rt, ks, red);
     if (wave != 0) return;
+    if (ad.direct) {
+      uint64_t *to = ad.ex + 2 * (((int64_t)ks * T + li) * ad.rp + 16 * rt + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t bits = __float_as_uint(u[i]);
+        if (li < T) {
+          st_dev_u64(to + 2 * i, tagged(bits, tag));
+          st_dev_u64(to + 2 * i + 1, tagged(bits >> 16, tag));
+        }
+      }
+      return;
+    }
     if (ad.slices > 1) {
       float *mine = ad.partial + (int64_t)rt * ad.slices * 256 + lane;
 #pragma unroll
@@ -650,6 +667,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
     }
     return;
   }
+  const bool first = (int)blockIdx.x == producers;
   const int64_t n0 = (int64_t)(blockIdx.x - producers) * 16;
   const int nb = (K + kStep - 1) / kStep;
   const rsrc_t wr = make_rsrc(W + n0 * K, (int64_t)16 * K), xr = make_rsrc(xq, (int64_t)T * K);
@@ -688,25 +706,49 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
   }
   if (producers) {
     constexpr int kAll = 64 * kStreamWaves, kPoll = 4;  // words of a thread asked for at once
-    const int tiles = ad.rp / 16, words = T * ad.rp;
+    const int tiles = ad.rp / 16, values = T * ad.rp;
+    const uint64_t mark = tagged(0u, tag) >> 16;
     if (tid < tiles) missing[tid] = 0u;
     __syncthreads();
     const long long t0 = wall_clock64(), limit = wait_limit(ad.counters + kMaxCounters - 1);
-    for (int e0 = tid; e0 < words; e0 += kAll * kPoll) {
+    if (ad.direct) {
+      float *const part = reinterpret_cast<float *>(red);
+      while (tid < values * ad.slices) {
+        const uint64_t lo = ld_dev_u64(ad.ex + 2 * tid), hi = ld_dev_u64(ad.ex + 2 * tid + 1);
+        if ((lo >> 16) == mark && (hi >> 16) == mark) {
+          part[tid] = __uint_as_float((uint32_t)hi << 16 | ((uint32_t)lo & 0xffffu));
+          break;
+        }
+        if (wall_clock64() - t0 > limit) {
+          missing[tid % ad.rp / 16] = 1u;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
+      }
+      __syncthreads();
+      if (tid < values) {
+        const int t = tid / ad.rp, j = tid - t * ad.rp;
+        float u = 0.f;
+        for (int ks = 0; ks < ad.slices; ++ks) u += part[ks * values + tid];
+        su[t * kSuPitch + j] = (uint16_t)pack_bf16x2(u * ad.scale, 0.f);
+        if (ad.u_out && first && j < ad.r) ad.u_out[t * ad.r + j] = u;
+      }
+    }
+    for (int e0 = tid; !ad.direct && e0 < values; e0 += kAll * kPoll) {
       for (;;) {
         uint64_t v[kPoll];
         bool all = true;
 #pragma unroll
-        for (int u = 0; u < kPoll; ++u) v[u] = e0 + u * kAll < words ? ld_dev_u64(ad.ex + e0 + u * kAll) : tagged(0u, tag);
+        for (int u = 0; u < kPoll; ++u) v[u] = e0 + u * kAll < values ? ld_dev_u64(ad.ex + e0 + u * kAll) : mark << 16;
 #pragma unroll
-        for (int u = 0; u < kPoll; ++u) all = all && (v[u] >> 16) == (tagged(0u, tag) >> 16);
+        for (int u = 0; u < kPoll; ++u) all = all && (v[u] >> 16) == mark;
         const bool late = !all && wall_clock64() - t0 > limit;
         if (all || late) {
 #pragma unroll
           for (int u = 0; u < kPoll; ++u) {
             const int e = e0 + u * kAll, t = e / ad.rp, j = e - t * ad.rp;
-            if (e >= words) continue;
-            if ((v[u] >> 16) == (tagged(0u, tag) >> 16))
+            if (e >= values) continue;
+            if ((v[u] >> 16) == mark)
               su[t * kSuPitch + j] = (uint16_t)v[u];
             else
               missing[j / 16] = 1u;
@@ -725,6 +767,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
       if (wave == 0 && li < T)
         *reinterpret_cast<u32x2 *>(su + li * kSuPitch + 16 * rt + 4 * g) =
             u32x2{pack_bf16x2(u[0] * ad.scale, u[1] * ad.scale), pack_bf16x2(u[2] * ad.scale, u[3] * ad.scale)};
+      if (ad.direct && ad.u_out && first && wave == 0 && li < T && 16 * rt + 4 * g < ad.r)
+        *reinterpret_cast<f32x4 *>(ad.u_out + li * ad.r + 16 * rt + 4 * g) = u;
       __syncthreads();
     }
     // rank columns in steps of 32, one per wave (r <= 256)
@@ -836,16 +880,19 @@ size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? kTileN * 64 * p.mj : kSmN * kSmT);
 }
 
-// the tagged values, then the slices' partials
-size_t fp8_stream_exchange_bytes(int rp) { return (size_t)16 * rp * 8 + (size_t)rp / 16 * kUSlices * 256 * 4; }
+// the tagged values (at least 2 kDirect words), then the slices' partials
+namespace {
+size_t exchange_words(int rp) { return (size_t)std::max(16 * rp, 2 * kDirect); }
+}  // namespace
+size_t fp8_stream_exchange_bytes(int rp) { return exchange_words(rp) * 8 + (size_t)rp / 16 * kUSlices * 256 * 4; }
 
 hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64_t K, const uint8_t *xq, const float *xs,
                              bool e5m2, int64_t T, const uint16_t *x, const uint16_t *A, const uint16_t *B, int r, int rp,
                              float scale, float *u_out, void *ex, uint32_t *counters, uint16_t *out,
                              hipStream_t st) {
   const int slices = (int)std::min<int64_t>(kUSlices, (K + 1023) / 1024);
-  const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, static_cast<uint64_t *>(ex),
-                         reinterpret_cast<float *>(static_cast<uint8_t *>(ex) + (size_t)16 * rp * 8), counters};
+  const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, T * rp * slices <= kDirect, static_cast<uint64_t *>(ex),
+                         reinterpret_cast<float *>(static_cast<uint64_t *>(ex) + exchange_words(rp)), counters};
   const int producers = r > 0 ? rp / 16 * slices : 0;
   const dim3 grid((unsigned)(N / 16 + producers)), block(64 * kStreamWaves);
   if (e5m2)
