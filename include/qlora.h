@@ -350,7 +350,8 @@ int qlora_fp8_forward(const qlora_fp8_weight *W, const uint8_t *xq, const float 
 /*
  * Backward through the frozen 8-bit base: dX = dYq W_hat + (alpha/r) v A with dY
  * quantized within the call to fmt along d_out (the adapter terms use dY
- * itself), v, dA and dB as in qlora_backward. No gradient flows into W.
+ * itself), v, dA and dB as in qlora_backward, the float32 u and v entering dB
+ * and dA with all their 24 bits. No gradient flows into W.
  * Arguments as for qlora_backward. Errors: as qlora_fp8_forward.
  */
 int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint16_t *dY, int fmt, int64_t T,

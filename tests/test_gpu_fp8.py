@@ -217,6 +217,28 @@ def test_adapter_gradients_keep_float32(T, N, K, r):
             assert dB is None
 
 
+@pytest.mark.parametrize("T,r", [(40, 8), (300, 64)])
+def test_adapter_gradients_of_the_largest_values(T, r):
+    """u at the end of float32's range, infinite and NaN: products as the formula has them, in their own column only."""
+    say(f"fp8 adapter gradients, large values T={T} r={r}")
+    g = _gen("large", T)
+    N = K = 272
+    w, x = _weight(g, N, K), _rows(g, T, K)
+    A, B = _adapter(g, N, K, r)
+    dY = torch.exp2(torch.randint(-12, -8, (T, N), generator=g, device="cuda").float()).bfloat16()
+    u = _randn(g, T, r)
+    plain = q.qlora_fp8_backward(w, x, dY, A, B, float(r), u_saved=u, need_dx=False, need_dA=False)[2]
+    u[:, 1] = 0
+    u[3, 1] = torch.finfo(torch.float32).max
+    u[5, 2] = float("inf")
+    u[7, 4] = float("nan")
+    dB = q.qlora_fp8_backward(w, x, dY, A, B, float(r), u_saved=u, need_dx=False, need_dA=False)[2]
+    assert torch.equal(dB[:, 1], u[3, 1] * dY[3].float())  # a power of two times it: exact
+    assert (dB[:, 2] == float("inf")).all() and torch.isnan(dB[:, 4]).all()
+    rest = [j for j in range(r) if j not in (1, 2, 4)]
+    assert torch.equal(dB[:, rest], plain[:, rest])
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_what_the_matrix_unit_keeps(fmt):
     """A large product and its negative beside a small one: among the same eight k the small one survives down to
