@@ -505,3 +505,70 @@ def test_backward_past_32_bit_offsets():
     V, Xd, Dd, U, lim = V[-300:], x[-300:].double(), dY[-300:].double(), u[-300:].double(), 2 * 308 * 2.0 ** -23
     _check("dA of the last", dA, da.double(), (lim * V.abs() + 2 * (N + 4) * 2.0 ** -23 * Vb[-300:]).t() @ Xd.abs())
     _check("dB of the last", dB, db.double(), lim * Dd.abs().t() @ U.abs())
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 1 << 20, 16), (1, 16, 1 << 20), (40, 1 << 20, 32), (40, 32, 1 << 20), (300, 16, 1 << 20),
+                                   (1 << 24, 16, 16)])
+def test_the_largest_sizes(T, N, K):
+    say(f"fp8 largest T={T} {N}x{K}")
+    g = _gen(T, N, K, "most")
+    w = _weight(g, N, K)
+    x = torch.randn(T, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    dY = torch.randn(T, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    A, B = _adapter(g, N, K, 8)
+    at = _some_rows(T) if T > 1000 else torch.arange(T, device="cuda")
+    Ad, Bd, wh = A.double(), B.double(), R.restored_weight(w.codes, w.scales)
+    h, u = q.qlora_fp8_forward(w, x, A, B, 8.0, save_u=True)
+    dX, dA, dB = q.qlora_fp8_backward(w, x, dY, A, B, 8.0, u_saved=u)
+    for rows, got, W_, P, Q in ((x, h, wh, Ad, Bd.t()), (dY, dX, wh.t(), Bd.t(), Ad)):
+        width = rows.shape[1]
+        codes, scales = R.quantize_rows(rows[at], R.E4M3)
+        xh, X = codes * R.spread_cols(scales, width), rows[at].double()
+        v, vb = X @ P.t(), (width + 4) * 2.0 ** -23 * (X.abs() @ P.abs().t())
+        ref = xh @ W_.t() + v @ Q
+        extra = (2.0 ** -8 * v.abs() + (1 + 2.0 ** -8) * vb) @ Q.abs() + 12 * 2.0 ** -23 * v.abs() @ Q.abs()
+        _check("h" if rows is x else "dX", got[at], ref, R.product_bound(xh, W_, ref, extra))
+    lim = (T + 8) * 2.0 ** -23
+    D, U, X = dY.double(), u.double(), x.double()
+    _check("dB", dB, D.t() @ U, D.abs().t() @ (lim * U.abs()))
+    V, vb = D @ Bd, (N + 4) * 2.0 ** -23 * (D.abs() @ Bd.abs())
+    _check("dA", dA, V.t() @ X, (lim * V.abs() + vb).t() @ X.abs())
+
+
+def test_backward_on_two_streams_and_one_workspace_in_turn():
+    """Backward calls that overlap, each with a workspace of its own; then one workspace for the 4-bit and the 8-bit
+    base's calls in turn, few tokens after many: every result as with a fresh workspace."""
+    say("fp8 backward on two streams, one workspace for both bases")
+    g = _gen("turns")
+    jobs = []
+    for T, N, K, r in ((333, 1024, 2048, 16), (200, 2048, 784, 64)):
+        w, x, dY = _weight(g, N, K), _rows(g, T, K), _rows(g, T, N)
+        A, B = _adapter(g, N, K, r)
+        ws = torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, r), dtype=torch.uint8, device="cuda")
+        jobs.append(((w, x, dY, A, B, 16.0), ws, q.qlora_fp8_backward(w, x, dY, A, B, 16.0)))
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in jobs], []
+    for _ in range(4):
+        for st, (args, ws, _) in zip(streams, jobs):
+            with torch.cuda.stream(st):
+                outs.append(q.qlora_fp8_backward(*args, ws=ws))
+    torch.cuda.synchronize()
+    for i, got in enumerate(outs):
+        assert all(torch.equal(a, b) for a, b in zip(got, jobs[i % 2][2]))
+
+    N, K, r = 1024, 2048, 64
+    W = _randn(g, N, K) * 0.02
+    w8, w4 = q.qlora_fp8_quantize(W), q.qlora_quantize(W)
+    A, B = _adapter(g, N, K, r)
+    T = 200
+    need = max(f(N, K, t, r) for f in (q.qlora_fp8_workspace_bytes, q.qlora_workspace_bytes) for t in (1, 4, 16, T))
+    shared = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for k in range(2):
+        for t in (T, 1, 4, T, 16, 2):
+            x = _rows(g, t, K)
+            for f, w in ((q.qlora_forward, w4), (q.qlora_fp8_forward, w8)):
+                fresh = torch.zeros(need, dtype=torch.uint8, device="cuda")
+                want = f(w, x, A, B, 16.0, save_u=True, ws=fresh)
+                got = f(w, x, A, B, 16.0, save_u=True, ws=shared)
+                assert all(torch.equal(a, b) for a, b in zip(got, want)), (k, t)
+    assert not shared[:q.COUNTER_BYTES].any()
