@@ -25,7 +25,7 @@ MARSHAL = os.path.join(HERE, "_marshal.so")
 MARSHAL_SOURCE = "binding.cpp"  # host code over torch's tensors and the C ABI
 
 SOURCES = ["api.cpp", "quantize.hip", "lora_small.hip", "gemv.hip", "gemm.hip", "lora_grad.hip", "lora_wide.hip", "merge.hip", "adamw.hip", "adamw_host.cpp", "scratch.hip", "api_ops.cpp",
-           "fp8_quant.hip", "fp8_gemm.hip", "adapter_grad.hip", "rmsnorm.hip", "adamw_many.hip"]
+           "fp8_quant.hip", "fp8_rows.hip", "fp8_gemm.hip", "adapter_grad.hip", "rmsnorm.hip", "adamw_many.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

@@ -32,7 +32,7 @@ int64_t groups(int64_t d) { return ceil_div(d, QLORA_FP8_GROUP); }
 // first, as in every workspace; q8 and qs hold the rows quantized within the
 // call, lt the adapter matrix that is contracted over its other dimension.
 struct Fp8Layout {
-  size_t ex, su, u, v, bt, lt, q8, qs, partial, total;
+  size_t ex, su, u, v, lt, q8, qs, partial, total;
 };
 Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   Fp8Layout L{};
@@ -48,18 +48,13 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   L.su = take((size_t)std::max<int64_t>(16, ceil_div(T, 16) * 16) * rp * 2);
   L.u = take((size_t)T * r * 4);
   L.v = take((size_t)T * r * 4);
-  L.bt = take((size_t)r * d_out * 2);
   L.lt = take((size_t)r * d_in * 2);
   L.q8 = take((size_t)T * d);
   L.qs = take((size_t)T * groups(d) * 4);
   size_t pf = 0;
   if (r > 0) {
-    if (T < kWideMinTokens) {
-      pf = std::max(pf, (size_t)ceil_div(T, 16) * lora_small_ksplit(T, d) * 16 * rp);
-    } else {
-      pf = std::max(pf, lora_tall_partial_floats(T, d_in, rp));
-      pf = std::max(pf, lora_tall_partial_floats(T, d_out, rp));
-    }
+    pf = std::max(pf, fp8_rows_partial_floats(T, d_in, rp));
+    pf = std::max(pf, fp8_rows_partial_floats(T, d_out, rp));
     pf = std::max(pf, adapter_grad_partial_floats(d_in, d_out, r, T));
   }
   pf = std::max(pf, fp8_partial_floats(T, d_out, d_in, false));
@@ -67,15 +62,6 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
   L.partial = take(pf * 4);
   L.total = off;
   return L;
-}
-
-// out_f32 = P Q^T and out_bf16 = bf16(scale * that), P [T, K], Q [r, K] (the adapter products of the 4-bit layer).
-hipError_t adapter_product(const uint16_t *P, const uint16_t *Q, int64_t T, int64_t K, int r, float scale, float *out_f32,
-                           uint16_t *out_bf16, float *partial, uint32_t *counters, hipStream_t st) {
-  if (T >= kWideMinTokens)
-    return launch_lora_tall(P, Q, T, K, r, rank_pad(r), scale, out_f32, out_bf16, partial, counters, st);
-  return launch_lora_small(P, Q, T, K, r, scale, out_f32, out_bf16, rank_pad(r), partial, counters,
-                           lora_small_ksplit(T, K), st);
 }
 
 int check_workspace(const void *ws, size_t ws_bytes, size_t need) {
@@ -134,28 +120,28 @@ int qlora_fp8_forward(const qlora_fp8_weight *W, const uint8_t *xq, const float 
     return QLORA_ERR_ALIGN;
   const Fp8Layout L = fp8_layout(W->d_out, W->d_in, T, r);
   if ((s = check_workspace(ws, ws_bytes, L.total))) return s;
+  const bool stream_kernel = T <= kFp8StreamTokens;  // which forms x A^T itself
+  const float sc = r > 0 ? alpha / (float)r : 0.f;
+  uint8_t *q = xq ? nullptr : at<uint8_t>(ws, L.q8);
+  float *qs = at<float>(ws, L.qs), *partial = at<float>(ws, L.partial);
+  uint16_t *su = at<uint16_t>(ws, L.su);
+  uint32_t *counters = at<uint32_t>(ws, 0);
   hipError_t e = hipSuccess;
-  if (!xq) {
-    uint8_t *q = at<uint8_t>(ws, L.q8);
-    float *qs = at<float>(ws, L.qs);
+  if (r > 0 && !stream_kernel)
+    e = launch_fp8_rows({x, T, W->d_in, q, qs, A, r, sc, u_out, su, nullptr, nullptr, 0, partial, counters}, fmt, false,
+                        rank_pad(r), stream);
+  else if (q)
     e = launch_fp8_quantize_rows(x, true, T, W->d_in, fmt == QLORA_E5M2, q, qs, stream);
-    if (e != hipSuccess) return QLORA_ERR_HIP;
+  if (e != hipSuccess) return QLORA_ERR_HIP;
+  if (q) {
     xq = q;
     xs = qs;
   }
-  if (T <= kFp8StreamTokens)
+  if (stream_kernel)
     return hip_status(launch_fp8_stream(W->codes, W->scales, W->d_out, W->d_in, xq, xs, fmt == QLORA_E5M2, T, x, A, B, r,
-                                        rank_pad(r), r > 0 ? alpha / (float)r : 0.f, u_out, at<uint8_t>(ws, L.ex),
-                                        at<uint32_t>(ws, 0), h, stream));
-  uint16_t *su = at<uint16_t>(ws, L.su);
-  if (r > 0) {
-    e = adapter_product(x, A, T, W->d_in, r, alpha / (float)r, u_out, su, at<float>(ws, L.partial), at<uint32_t>(ws, 0),
-                        stream);
-    if (e != hipSuccess) return QLORA_ERR_HIP;
-  }
+                                        rank_pad(r), sc, u_out, at<uint8_t>(ws, L.ex), counters, h, stream));
   return hip_status(launch_fp8_product(W->codes, W->scales, W->d_out, W->d_in, false, xq, xs, fmt == QLORA_E5M2, T, su,
-                                       rank_pad(r), B, r, h, at<float>(ws, L.partial), at<uint32_t>(ws, 0),
-                                       stream));
+                                       rank_pad(r), B, r, h, partial, counters, stream));
 }
 
 int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint16_t *dY, int fmt, int64_t T,
@@ -184,16 +170,21 @@ int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint1
   uint32_t *counters = at<uint32_t>(ws, 0), *fallbacks = counters + kMaxCounters - 1;
   uint8_t *q = dX ? at<uint8_t>(ws, L.q8) : nullptr;
   float *qs = at<float>(ws, L.qs);
-  uint16_t *bt = r > 0 && (dX || dA) ? at<uint16_t>(ws, L.bt) : nullptr, *lt = r > 0 && dX ? at<uint16_t>(ws, L.lt) : nullptr;
-  hipError_t e = launch_fp8_prepare_backward(dY, T, d_out, d_in, fmt == QLORA_E5M2, q, qs, A, B, r, lt, bt, stream);
-  if (e == hipSuccess && bt) e = adapter_product(dY, bt, T, d_out, r, sc, v, sv, partial, counters, stream);
+  uint16_t *lt = r > 0 && dX ? at<uint16_t>(ws, L.lt) : nullptr;
+  hipError_t e = hipSuccess;
+  if (r > 0 && (dX || dA))
+    e = launch_fp8_rows({dY, T, d_out, q, qs, B, r, sc, v, sv, A, lt, d_in, partial, counters}, fmt, true, rank_pad(r),
+                        stream);
+  else if (dX)
+    e = launch_fp8_quantize_rows(dY, true, T, d_out, fmt == QLORA_E5M2, q, qs, stream);
   if (e == hipSuccess && dX)
     e = launch_fp8_product(W->codes, W->scales, d_out, d_in, true, q, qs, fmt == QLORA_E5M2, T, sv, rank_pad(r), lt, r,
                            dX, partial, counters, stream);
   const float *u = u_saved;
   if (e == hipSuccess && dB && !u) {
     u = at<float>(ws, L.u);
-    e = adapter_product(x, A, T, d_in, r, 1.f, at<float>(ws, L.u), nullptr, partial, counters, stream);
+    e = launch_fp8_rows({x, T, d_in, nullptr, nullptr, A, r, 1.f, at<float>(ws, L.u), nullptr, nullptr, nullptr, 0, partial,
+                         counters}, fmt, false, rank_pad(r), stream);
   }
   if (e == hipSuccess)
     e = launch_adapter_grad({x, v, dA, d_in}, {dY, u, dB, d_out}, T, r, sc, partial, counters, fallbacks, stream);

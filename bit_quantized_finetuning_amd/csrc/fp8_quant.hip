@@ -2,8 +2,8 @@
 // groups of 128 with a power-of-two scale, weights in blocks of 128 x 128 with
 // scale amax / 448.
 //
-// The backward's call also transposes its adapter's matrices in the launch that
-// quantizes dY (a launch of its own for each took 3 to 5 us of a short backward).
+// Rows whose call also multiplies them with an adapter are quantized in the same
+// pass as that product (fp8_rows.hip), by the same rule.
 //
 // Both quantizers read every value once and write one byte for it, so HBM bounds them: 3
 // bytes per value from bf16. The group maximum of a row is taken over 16 lanes
@@ -40,75 +40,24 @@ __device__ __forceinline__ float amax8(const float v[8]) {
 // One workgroup per unit of 2048 consecutive columns of one row (16 groups);
 // d % 8 == 0, so a lane's 8 values are all inside the row or all outside.
 template <typename E, bool E5M2>
-__device__ __forceinline__ void quantize_unit(const E *__restrict__ x, int64_t u, int upr, int d,
-                                              uint8_t *__restrict__ codes, float *__restrict__ scales) {
-  const int tid = threadIdx.x, ng = (d + kFp8Group - 1) / kFp8Group;
-  const int64_t row = u / upr;
-  const int col = (int)(u - row * upr) * 2048 + tid * 8;
-  const bool in = col < d;
-  float v[8] = {};
-  if (in) load8(x + row * d + col, v);
-  const RowScale sc = row_scale<E5M2>(max16(amax8(v)));
-  if (in) {
-    u32x2 q;
-    q[0] = pack_fp8x4<E5M2>(v[0] * sc.inv, v[1] * sc.inv, v[2] * sc.inv, v[3] * sc.inv);
-    q[1] = pack_fp8x4<E5M2>(v[4] * sc.inv, v[5] * sc.inv, v[6] * sc.inv, v[7] * sc.inv);
-    *reinterpret_cast<u32x2 *>(codes + row * d + col) = q;
-    if ((tid & 15) == 0) scales[row * ng + col / kFp8Group] = sc.s;
-  }
-}
-template <typename E, bool E5M2>
 __global__ __launch_bounds__(256) void k_fp8_quantize_rows(const E *__restrict__ x, int64_t units, int upr, int d,
                                                            uint8_t *__restrict__ codes, float *__restrict__ scales) {
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) quantize_unit<E, E5M2>(x, u, upr, d, codes, scales);
-}
-
-// 32 x 32 elements of a transpose; r >= 8, so at most 2^17 tiles of either matrix
-__device__ __forceinline__ void transpose_tile(const uint16_t *__restrict__ src, int64_t rows, int64_t cols, int tile,
-                                               uint16_t *__restrict__ dst, uint16_t (*t)[33]) {
-  const int tc = (int)((cols + 31) / 32), tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t r0 = (int64_t)(tile / tc) * 32, c0 = (int64_t)(tile % tc) * 32;
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    t[ty + i][tx] = r0 + ty + i < rows && c0 + tx < cols ? src[(r0 + ty + i) * cols + c0 + tx] : (uint16_t)0;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    if (c0 + ty + i < cols && r0 + tx < rows) dst[(c0 + ty + i) * rows + r0 + tx] = t[tx][ty + i];
-}
-
-// The backward's inputs in one launch: first the tiles of the two transposes, then the units of dY.
-template <bool E5M2>
-__global__ __launch_bounds__(256) void k_fp8_prepare_backward(const uint16_t *__restrict__ dY, int64_t units, int upr,
-                                                              int64_t d_out, int64_t d_in, uint8_t *__restrict__ codes,
-                                                              float *__restrict__ scales,
-                                                              const uint16_t *__restrict__ A,
-                                                              const uint16_t *__restrict__ B, int r,
-                                                              uint16_t *__restrict__ lt, uint16_t *__restrict__ bt,
-                                                              int tiles_a, int tiles_b) {
-  __shared__ uint16_t t[32][33];
-  const int tiles = tiles_a + tiles_b;
-  if ((int)blockIdx.x < tiles_a) return transpose_tile(A, r, d_in, blockIdx.x, lt, t);
-  if ((int)blockIdx.x < tiles) return transpose_tile(B, d_out, r, blockIdx.x - tiles_a, bt, t);
-  for (int64_t u = blockIdx.x - tiles; u < units; u += gridDim.x - tiles)
-    quantize_unit<uint16_t, E5M2>(dY, u, upr, (int)d_out, codes, scales);
-}
-
-hipError_t launch_fp8_prepare_backward(const uint16_t *dY, int64_t T, int64_t d_out, int64_t d_in, bool e5m2,
-                                       uint8_t *codes, float *scales, const uint16_t *A, const uint16_t *B, int r,
-                                       uint16_t *lt, uint16_t *bt, hipStream_t st) {
-  const int upr = (int)((d_out + 2047) / 2048), tr = (r + 31) / 32;
-  const int64_t units = codes ? T * upr : 0;
-  const int ta = lt ? tr * (int)((d_in + 31) / 32) : 0, tb = bt ? tr * (int)((d_out + 31) / 32) : 0;
-  const dim3 grid((unsigned)(ta + tb + (units < 65536 ? units : 65536)));
-  if (grid.x == 0) return hipSuccess;
-  if (e5m2)
-    k_fp8_prepare_backward<true><<<grid, dim3(256), 0, st>>>(dY, units, upr, d_out, d_in, codes, scales, A, B, r, lt, bt,
-                                                             ta, tb);
-  else
-    k_fp8_prepare_backward<false><<<grid, dim3(256), 0, st>>>(dY, units, upr, d_out, d_in, codes, scales, A, B, r, lt,
-                                                              bt, ta, tb);
-  return hipGetLastError();
+  const int tid = threadIdx.x, ng = (d + kFp8Group - 1) / kFp8Group;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t row = u / upr;
+    const int col = (int)(u - row * upr) * 2048 + tid * 8;
+    const bool in = col < d;
+    float v[8] = {};
+    if (in) load8(x + row * d + col, v);
+    const RowScale sc = row_scale<E5M2>(max16(amax8(v)));
+    if (in) {
+      u32x2 q;
+      q[0] = pack_fp8x4<E5M2>(v[0] * sc.inv, v[1] * sc.inv, v[2] * sc.inv, v[3] * sc.inv);
+      q[1] = pack_fp8x4<E5M2>(v[4] * sc.inv, v[5] * sc.inv, v[6] * sc.inv, v[7] * sc.inv);
+      *reinterpret_cast<u32x2 *>(codes + row * d + col) = q;
+      if ((tid & 15) == 0) scales[row * ng + col / kFp8Group] = sc.s;
+    }
+  }
 }
 
 hipError_t launch_fp8_quantize_rows(const void *x, bool bf16_in, int64_t T, int64_t d, bool e5m2, uint8_t *codes,

@@ -198,11 +198,28 @@ hipError_t launch_adapter_grad(const AdapterGradJob &a, const AdapterGradJob &b,
                                float *partial, uint32_t *counters, uint32_t *fallbacks, hipStream_t st);
 size_t adapter_grad_partial_floats(int64_t Da, int64_t Db, int R, int64_t T);
 
-// fp8_quant.hip: what the backward needs before its products, in one launch: the rows of dY [T, d_out] in 8 bits (codes
-// == NULL: not), B^T [r, d_out] (bt == NULL: not) and A^T [d_in, r] (lt == NULL: not).
-hipError_t launch_fp8_prepare_backward(const uint16_t *dY, int64_t T, int64_t d_out, int64_t d_in, bool e5m2,
-                                       uint8_t *codes, float *scales, const uint16_t *A, const uint16_t *B, int r,
-                                       uint16_t *lt, uint16_t *bt, hipStream_t st);
+// fp8_rows.hip: one pass over bf16 rows P [T, K] (K % 16 == 0): their 8-bit codes and scales (codes == NULL: not), and
+// out[T, r] = P Q^T with Q = A [r, K] or, q_is_b, B [K, r] (r % 8 == 0, r > 0): out_f32 [T, r] (nullable), out_bf16 =
+// bf16(scale out) [T, rp] (nullable, zero columns r .. rp - 1); and lt [d_lt, r] = A^T for A [r, d_lt] (lt == NULL: not).
+// Uses `partial` (fp8_rows_partial_floats) and `counters` (one tile_counter per 64 tokens or fewer).
+struct RowsJob {
+  const uint16_t *P;
+  int64_t T, K;
+  uint8_t *codes;
+  float *scales;
+  const uint16_t *Q;
+  int r;
+  float scale;
+  float *out_f32;
+  uint16_t *out_bf16;
+  const uint16_t *A;
+  uint16_t *lt;
+  int64_t d_lt;
+  float *partial;
+  uint32_t *counters;
+};
+hipError_t launch_fp8_rows(const RowsJob &a, int fmt, bool q_is_b, int rp, hipStream_t st);
+size_t fp8_rows_partial_floats(int64_t T, int64_t K, int rp);
 
 // fp8_quant.hip: rows [T, d] (d % 8 == 0) to 8 bits in groups of 128 with power-of-two scales [T, ceil(d / 128)];
 // a weight [N, K] (K % 8 == 0) to e4m3 in blocks of 128 x 128 with scales [ceil(N / 128), ceil(K / 128)].
