@@ -29,6 +29,10 @@ constexpr int kRwMaxSplit = 16;
 // lanes: rows q and 32 + q, q < 4) takes 256 consecutive bytes. rw_row is its inverse.
 __device__ __forceinline__ int rw_slot(int t) { return (t & 3) | ((t >> 5) & 1) << 2 | ((t >> 2) & 7) << 3 | (t & 64); }
 __device__ __forceinline__ int rw_row(int s) { return (s & 3) | ((s >> 3) & 7) << 2 | ((s >> 2) & 1) << 5 | (s & 64); }
+// Chunk c of a row of 256 bytes sits at c ^ rw_turn(row): a 16-byte read takes 16 lanes at a time, rows 0 .. 3 and 12 ..
+// 15 of one lane group with rows 4 .. 11 of the next, and these fall on 16 different chunks (with the row itself instead:
+// half of the LDS cycles were conflicts).
+__device__ __forceinline__ int rw_turn(int row) { return (row + 4) & 15; }
 
 // Stores issued from asm. (No write of their data registers follows within the wait state they need.)
 __device__ __forceinline__ void store16_asm(const i32x4 &rs, const u32x4 &v, uint32_t off) {
@@ -89,7 +93,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
   const i32x4 cr = rsrc_words(FMT ? a.codes + t0 * K : nullptr, FMT ? rows * K : 0);
   const i32x4 sr = rsrc_words(FMT ? a.scales + t0 * nk : nullptr, FMT ? rows * nk * 4 : 0);
 
-  // P: wave w's rows are 16 w .. +15 of the tile, 256 bytes each, 16-byte chunk c of row t at c ^ (t & 15); copy q takes
+  // P: wave w's rows are 16 w .. +15 of the tile, 256 bytes each, 16-byte chunk c of row t at c ^ rw_turn(t); copy q takes
   // rows 4 q .. +3 of them. Q by rows: 16 ranks' tiles of the same form; B's: [128][16] tiles by rw_slot. Copies of Q:
   // wave w takes KB w QC .. +QC-1. A chunk at or past K reads zeros, as do rows past T, r and K.
   uint32_t psrc[4], qsrc[QC];
@@ -97,7 +101,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int row = 4 * q + (lane >> 4);
-    pk[q] = 8 * ((lane & 15) ^ row);
+    pk[q] = 8 * ((lane & 15) ^ rw_turn(row));
     psrc[q] = (uint32_t)(((16 * wave + row) * K + pk[q]) * 2);
   }
 #pragma unroll
@@ -109,7 +113,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
       qsrc[j] = col < a.r ? (uint32_t)((row * a.r + col) * 2) : kOOB;
     } else {
       const int row = 4 * q + (lane >> 4);
-      qk[j] = 8 * ((lane & 15) ^ row);
+      qk[j] = 8 * ((lane & 15) ^ rw_turn(row));
       qsrc[j] = 16 * n + row < a.r ? (uint32_t)(((int64_t)(16 * n + row) * K + qk[j]) * 2) : kOOB;
     }
   }
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
     const uint8_t *ps = rsm + ((kt - k0) % RS) * kSlot, *qs = ps + kRwP;
     u32x4 p[4];
 #pragma unroll
-    for (int kk = 0; kk < 4; ++kk) p[kk] = ld16(ps + pfrag + (((4 * g + kk) ^ li) << 4));
+    for (int kk = 0; kk < 4; ++kk) p[kk] = ld16(ps + pfrag + (((4 * g + kk) ^ rw_turn(li)) << 4));
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -172,7 +176,7 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
           const u32x2 f1 = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(b + qfrag[1])));
           f = u32x4{f0[0], f0[1], f1[0], f1[1]};
         } else {
-          f = ld16(qs + 4096 * n + qfrag[0] + (((4 * g + kk) ^ li) << 4));
+          f = ld16(qs + 4096 * n + qfrag[0] + (((4 * g + kk) ^ rw_turn(li)) << 4));
         }
         acc[n] = mfma16(f, p[kk], acc[n]);
       }
