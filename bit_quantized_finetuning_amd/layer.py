@@ -137,6 +137,8 @@ def _deposit_fp32(p: torch.nn.Parameter, g: torch.Tensor):
 class _Bf16Module(torch.nn.Module):
     """Dtype casts leave the quantized storage and the bf16 adapters as they are; device moves apply."""
 
+    base = "nf4"  # of modules that do not say (a subclass's, or saved before there was a choice)
+
     def _apply(self, fn, recurse=True):
         def keep_dtype(t):
             moved = fn(t)
