@@ -17,20 +17,28 @@
 namespace qlora {
 
 // ---------------------------------------------------------------------------
-// The large-tile kernel: 256 outputs x 64 MJ tokens per workgroup of eight waves,
-// each 128 outputs x 16 MJ tokens (MJ = 4 for whole batches, 3 and 2 where a
-// narrower tile leaves fewer compute units idle); K advances by one scale block
-// of 128. Both operands' tiles go from memory straight into LDS (two tiles of
-// each, step k + 1 on its way during step k), as do the token scales. Measured:
+// The large-tile kernel: 32 MI outputs x 64 MJ tokens per workgroup of eight
+// waves, each 16 MI outputs x 16 MJ tokens; K advances by one scale block of 128.
+// Both operands' tiles go from memory straight into LDS (S tiles of each, steps
+// k + 1 .. k + S - 1 on their way during step k), as do the token scales.
+// 256 outputs x 256 tokens for whole batches, and 256 x 192, 192 x 192 (by rows)
+// or 256 x 128 where that leaves fewer compute units idle. With all of them at
+// work on 256 x 256 two stages keep up with the clock that power allows; the
+// smaller tiles' steps last as long as the copies take, so those that have room
+// for three stages have them (515 tokens, 13824 x 5120: 192 x 192 54 -> 48 us,
+// 256 x 128 92 -> 84). Measured:
 // 4096 tokens, 22016 x 8192: 641 us (2300 TFLOP/s) by rows, 633 by columns; the
 // matrix unit is busy half of the cycles, at the clock that power leaves it.
 // ---------------------------------------------------------------------------
-constexpr int kTileN = 256, kStep = 128;
-constexpr int kWaveN = 128;
-constexpr int kOperand = kTileN * kStep;              // bytes of one operand's tile
-constexpr int kStage = 2 * kOperand;                  // weight tile, token tile
+constexpr int kStep = 128;
 constexpr int kScales = 256 * 16;                     // four steps' token scales
-constexpr size_t kFp8Lds = (size_t)2 * kStage + 2 * kScales;
+
+template <bool TRANS, int MI, int MJ, int S>
+struct Fp8Lds {
+  static constexpr int w = TRANS ? 256 * kStep : 32 * MI * kStep;  // (by columns rows are always 256 bytes apart)
+  static constexpr int stage = w + 64 * MJ * kStep;
+  static constexpr int bytes = S * stage + 2 * kScales;
+};
 
 // One dword per lane from memory into LDS (lane L lands at M0 + 4 L).
 __device__ __forceinline__ void dma4_asm(const i32x4 &rs, uint32_t m0v, uint32_t voff, uint32_t soff) {
@@ -67,7 +75,7 @@ __device__ __forceinline__ WorkPlace work_place(int work, int gn, int gt, int pa
   return tile_place(xcd * share + (xcd < extra ? xcd : extra) + blockIdx.x / 8, gn, gt, parts);
 }
 
-template <bool TRANS, bool E5M2, int MJ>
+template <bool TRANS, bool E5M2, int MI, int MJ, int S>
 __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__ W, const float *__restrict__ ws,
                                                      int N, int K, int ldw, int sld, const uint8_t *__restrict__ xq,
                                                      const float *__restrict__ xs, int64_t T,
@@ -75,7 +83,9 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
                                                      const uint16_t *__restrict__ L, int r, int gn, int gt, int full,
                                                      int parts, float *__restrict__ partial,
                                                      uint32_t *__restrict__ counters, uint16_t *__restrict__ out) {
-  constexpr int kTileT = 64 * MJ, kWaveT = 16 * MJ;
+  constexpr int kTileN = 32 * MI, kWaveN = 16 * MI, kTileT = 64 * MJ, kWaveT = 16 * MJ;
+  using Lds = Fp8Lds<TRANS, MI, MJ, S>;
+  constexpr int QW = TRANS ? 4 : MI / 2, kStage = Lds::stage;  // KB of the weight tile per wave
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
@@ -94,44 +104,44 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   const int rows_t = T - t0 < kTileT ? (int)(T - t0) : kTileT;
   const int rows_n = N - n0 < kTileN ? (int)(N - n0) : kTileN;
 
-  // copies: wave w's piece q fills KB 4 w + q of the weight tile, KB MJ w + q of the token tile
+  // copies: wave w's piece q fills KB QW w + q of the weight tile, KB MJ w + q of the token tile
   const i32x4 xr = rsrc_words(xq + t0 * K, (int64_t)rows_t * K);
   const i32x4 sr = rsrc_words(xs + t0 * nb, (int64_t)rows_t * nb * 4);
   const i32x4 wr0 = rsrc_words(W + n0 * (TRANS ? 1 : (int64_t)ldw), TRANS ? 0 : (int64_t)rows_n * ldw);
-  uint32_t xv[MJ], wv[4];
+  uint32_t xv[MJ], wv[QW];
 #pragma unroll
   for (int q = 0; q < MJ; ++q) {
     const int row = 8 * (MJ * wave + q) + (lane >> 3);
     xv[q] = (uint32_t)(row * K + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = 8 * (4 * wave + q) + (lane >> 3);
+  for (int q = 0; q < QW; ++q) {
+    const int row = 8 * (QW * wave + q) + (lane >> 3);
     if constexpr (TRANS) {
-      const int k = 4 * (4 * wave + q) + (lane >> 4);
-      wv[q] = (uint32_t)(k * ldw + 16 * ((lane & 15) ^ ((k & 7) | (((k >> 4) & 1) << 3))));
+      const int k = 4 * (4 * wave + q) + (lane >> 4), c = 16 * ((lane & 15) ^ ((k & 7) | (((k >> 4) & 1) << 3)));
+      wv[q] = c < kTileN ? (uint32_t)(k * ldw + c) : kOOB;
     } else {
       wv[q] = (uint32_t)(row * ldw + 16 * ((lane & 7) ^ ((row >> 1) & 7)));
     }
   }
-  const uint32_t lds_w = lds_addr(smem) + 4096u * (uint32_t)wave;
-  const uint32_t lds_x = lds_addr(smem) + kOperand + 1024u * MJ * (uint32_t)wave;
+  const uint32_t lds_w = lds_addr(smem) + 1024u * QW * (uint32_t)wave;
+  const uint32_t lds_x = lds_addr(smem) + Lds::w + 1024u * MJ * (uint32_t)wave;
   // Column of the lane's chunk in even KB of a tile and, 64 further on or back, in odd ones. A chunk is whole or past
   // the range's end (K % 16 == 0); there it reads zeros, and so does every chunk of a step past the last.
   const int c0 = 16 * ((lane & 7) ^ ((lane >> 4) & 7)), c1 = c0 ^ 64;
   auto copy_x = [&](int b, int q) {
     const int k0 = b * kStep;
     const bool in = k0 + (((MJ * wave + q) & 1) ? c1 : c0) < klim;
-    dma16_asm(xr, lds_x + (uint32_t)((b & 1) * kStage + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
+    dma16_asm(xr, lds_x + (uint32_t)((b % S) * kStage + 1024 * q), in ? xv[q] + (uint32_t)k0 : kOOB, 0u);
   };
   auto copy_w = [&](int b, int q) {
     const int k0 = b * kStep;
-    const uint32_t to = lds_w + (uint32_t)((b & 1) * kStage + 1024 * q);
+    const uint32_t to = lds_w + (uint32_t)((b % S) * kStage + 1024 * q);
     if constexpr (TRANS) {
       const int left = klim - k0 < kStep ? klim - k0 : kStep;
       dma16_asm(rsrc_words(W + (int64_t)k0 * ldw + n0, left > 0 ? (int64_t)left * ldw - n0 : 0), to, wv[q], 0u);
     } else {
-      const bool in = k0 + ((q & 1) ? c1 : c0) < klim;
+      const bool in = k0 + (((QW * wave + q) & 1) ? c1 : c0) < klim;
       dma16_asm(wr0, to, in ? wv[q] + (uint32_t)k0 : kOOB, 0u);
     }
   };
@@ -142,7 +152,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
   auto scale_start = [&](int group) { return wide && 4 * group + 4 > nb ? nb - 4 : 4 * group; };
   auto copy_s = [&](int group) {
     if (wave >= MJ) return;
-    const uint32_t to = lds_addr(smem) + (uint32_t)(2 * kStage + (group & 1) * kScales);
+    const uint32_t to = lds_addr(smem) + (uint32_t)(S * kStage + (group & 1) * kScales);
     const uint32_t at = (uint32_t)((wave * 64 + lane) * nb + scale_start(group)) * 4u;
     if (wide) {
       dma16_asm(sr, to + 1024u * (uint32_t)wave, at, 0u);
@@ -151,27 +161,30 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     }
   };
 
-  f32x4 acc[8][MJ];
+  f32x4 acc[MI][MJ];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < MJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const uint32_t frag = (uint32_t)(li * 128 + ((g ^ ((li >> 1) & 7)) << 4));
   // columns by transposing reads: lane l of 16 points at 8 bytes of row l / 2, and gets the 8 rows of column l
   const uint32_t tr_row = (uint32_t)((16 * g + (li >> 1)) * 256 + (li & 1) * 8), tr_f = (uint32_t)((li >> 1) | ((g & 1) << 3));
-  // a wave past the last column reads the last block's scale: its results are not stored
-  const int64_t nblk = n0 / 128 + wn, nlast = (N - 1) / 128;
+  // A wave past the last column reads the last block's scale: its results are not stored. 96 outputs of a wave may lie in
+  // two blocks: those from i = turn on have the second scale.
+  const int64_t nblk = (n0 + wn * kWaveN) / 128, nlast = (N - 1) / 128;
   const float *wsp = ws + (nblk < nlast ? nblk : nlast) * (TRANS ? 1 : sld);
+  const float *wsp2 = ws + (nblk + 1 < nlast ? nblk + 1 : nlast) * (TRANS ? 1 : sld);
+  const int turn = MI == 8 ? 8 : (int)(128 * (nblk + 1) - (n0 + wn * kWaveN)) / 16;
   const int64_t wstep = TRANS ? sld : 1;
 
   auto load_x = [&](const uint8_t *st, int j) {
-    const uint8_t *t = st + kOperand + wt * (kWaveT * kStep) + j * 2048;
+    const uint8_t *t = st + Lds::w + wt * (kWaveT * kStep) + j * 2048;
     return join8(ld16(t + frag), ld16(t + (frag ^ 64u)));
   };
   auto load_w = [&](const uint8_t *st, int i) {
     if constexpr (TRANS) {
-      const uint8_t *t = st + tr_row + (((uint32_t)(wn * 8 + i) ^ tr_f) << 4);
+      const uint8_t *t = st + tr_row + (((uint32_t)(wn * MI + i) ^ tr_f) << 4);
       i32x8 w;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -187,72 +200,87 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     }
   };
   auto load_s = [&](int b, int j) {
-    const uint8_t *t = smem + 2 * kStage + ((b >> 2) & 1) * kScales + (b - scale_start(b >> 2)) * s_step;
+    const uint8_t *t = smem + S * kStage + ((b >> 2) & 1) * kScales + (b - scale_start(b >> 2)) * s_step;
     return *reinterpret_cast<const float *>(t + (wt * kWaveT + j * 16 + li) * s_tok);
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   i32x8 xf[MJ], w0;
-  float sc[MJ];
+  float sc[MJ], sc2[MJ];
   auto add = [&](const f32x4 &p, int i, int j) {
+    const float s = MI == 8 || i < turn ? sc[j] : sc2[j];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sc[j], acc[i][j][e]);
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], s, acc[i][j][e]);
     pin(acc[i][j]);  // (or the sums sink past the branches of the copy, and every product waits in registers)
   };
 
 #pragma unroll
-  for (int q = 0; q < 4; ++q) copy_w(b0, q);
+  for (int q = 0; q < QW; ++q) copy_w(b0, q);
 #pragma unroll
   for (int q = 0; q < MJ; ++q) copy_x(b0, q);
   copy_s(b0 >> 2);
-  wait_barrier<0>();
+  if constexpr (S == 3) {
 #pragma unroll
-  for (int q = 0; q < MJ; ++q) copy_x(b0 + 1, q);
-  float wsc = wsp[b0 * wstep];
-  const uint8_t *first = smem + (size_t)(b0 & 1) * kStage;
+    for (int q = 0; q < QW; ++q) copy_w(b0 + 1, q);
+#pragma unroll
+    for (int q = 0; q < MJ; ++q) copy_x(b0 + 1, q);
+  }
+  wait_barrier<(S - 2) * (QW + MJ)>();
+#pragma unroll
+  for (int q = 0; q < MJ; ++q) copy_x(b0 + S - 1, q);
+  float wsc = wsp[b0 * wstep], wsc2 = MI == 8 ? 0.f : wsp2[b0 * wstep];
+  const uint8_t *first = smem + (size_t)(b0 % S) * kStage;
 #pragma unroll
   for (int j = 0; j < MJ; ++j) {
     xf[j] = load_x(first, j);
-    sc[j] = load_s(b0, j) * wsc;
+    const float sx = load_s(b0, j);
+    sc[j] = sx * wsc;
+    sc2[j] = sx * wsc2;
   }
   w0 = load_w(first, 0);
 
   for (int b = b0; b < b1; ++b) {
-    const uint8_t *st = smem + (size_t)(b & 1) * kStage, *next = smem + (size_t)((b & 1) ^ 1) * kStage;
+    const uint8_t *st = smem + (size_t)(b % S) * kStage, *next = smem + (size_t)((b + 1) % S) * kStage;
     i32x8 wf[3];
     wf[0] = w0;
     f32x4 p[2][MJ];
-    // outputs 16 i .. +15 of the wave, i = 0 .. 5: four products, the sums of the i before, the weights of the i after
+    // outputs 16 i .. +15 of the wave, all but the last two i: the products, the sums of the i before, the weights of the
+    // i after
+    constexpr int IL = MI - 3;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i <= IL; ++i) {
       wf[(i + 1) % 3] = load_w(st, i + 1);
-      if (i == 5) wf[1] = load_w(st, 7);
-      if (i == 3) wsc = wsp[(b + 1 < b1 ? b + 1 : b) * wstep];
+      if (i == IL) wf[(IL + 2) % 3] = load_w(st, IL + 2);
+      if (i == IL - 2) {
+        wsc = wsp[(b + 1 < b1 ? b + 1 : b) * wstep];
+        if constexpr (MI < 8) wsc2 = wsp2[(b + 1 < b1 ? b + 1 : b) * wstep];
+      }
 #pragma unroll
       for (int j = 0; j < MJ; ++j) {
         p[i & 1][j] = mfma_fp8<E5M2>(wf[i % 3], xf[j], zero);
         QLORA_SCHED_FENCE();
-        // (sent early in the step, two to a group: the last must land before its end)
-        if (MJ == 4 ? i < 2 && (j & 1) : i < 4 && j == 1) copy_w(b + 1, MJ == 4 ? 2 * i + (j >> 1) : i);
+        // (sent early in the step, two to a group where there are four: the last must land before its end)
+        const int q = MJ == 4 ? 2 * i + (j >> 1) : i;
+        if (q < QW && (MJ == 4 ? (j & 1) : j == 1)) copy_w(b + S - 1, q);
         if (i > 0) add(p[(i & 1) ^ 1][j], i - 1, j);
         QLORA_SCHED_FENCE();
       }
     }
     // every fragment of this step is in registers: the next step's tiles are awaited and the one after is sent for
-    // while i = 6, 7 are still to be multiplied
-    wait_barrier<0>();
+    // while the last two i are still to be multiplied (three stages: the newest QW + MJ copies are of the step after)
+    wait_barrier<(S - 2) * (QW + MJ)>();
     if ((b & 3) == 0 && b + 4 < b1) copy_s((b >> 2) + 1);
     QLORA_SCHED_FENCE();
     f32x4 q6, q7;
     float sn[MJ];
 #pragma unroll
     for (int j = 0; j < MJ; ++j) {
-      const f32x4 a6 = mfma_fp8<E5M2>(wf[0], xf[j], zero), a7 = mfma_fp8<E5M2>(wf[1], xf[j], zero);
+      const f32x4 a6 = mfma_fp8<E5M2>(wf[(IL + 1) % 3], xf[j], zero), a7 = mfma_fp8<E5M2>(wf[(IL + 2) % 3], xf[j], zero);
       QLORA_SCHED_FENCE();
-      copy_x(b + 2, j);
-      add(p[1][j], 5, j);
+      copy_x(b + S, j);
+      add(p[IL & 1][j], IL, j);
       if (j > 0) {
-        add(q6, 6, j - 1);
-        add(q7, 7, j - 1);
+        add(q6, IL + 1, j - 1);
+        add(q7, IL + 2, j - 1);
       }
       q6 = a6;
       q7 = a7;
@@ -261,21 +289,24 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       if (j == 1) w0 = load_w(next, 0);
       QLORA_SCHED_FENCE();
     }
-    add(q6, 6, MJ - 1);
-    add(q7, 7, MJ - 1);
+    add(q6, IL + 1, MJ - 1);
+    add(q7, IL + 2, MJ - 1);
 #pragma unroll
-    for (int j = 0; j < MJ; ++j) sc[j] = sn[j] * wsc;
+    for (int j = 0; j < MJ; ++j) {
+      sc[j] = sn[j] * wsc;
+      sc2[j] = sn[j] * wsc2;
+    }
   }
 
   wait_vmem();  // no copy into LDS outlives the workgroup
 
   if (cut) {
     // [part][group of four floats][thread]: one 16-byte store each, whole lines per wave
-    constexpr int kGroups = 8 * MJ, kPart = kGroups * 512 * 16;
+    constexpr int kGroups = MI * MJ, kPart = kGroups * 512 * 16;
     float *mine = partial + ((int64_t)tail * parts + part) * (kPart / 4);
     const rsrc_t pr = make_rsrc(mine, kPart);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < MJ; ++j)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), pr,
@@ -293,7 +324,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     // the last to arrive adds the ranges in order, its own from its registers
     const rsrc_t all = make_rsrc(partial + (int64_t)tail * parts * (kPart / 4), (int64_t)parts * kPart);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
+    for (int i = 0; i < MI; i += 2) {
       f32x4 sum[2 * MJ];
 #pragma unroll
       for (int q = 0; q < 2 * MJ; ++q) sum[q] = zero;
@@ -326,7 +357,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
       if (k < r && tw + j * 16 + li < T) sf[j] = ld16(su + (tw + j * 16 + li) * rp + k);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < MI; ++i) {
       u32x4 lf = {0, 0, 0, 0};
       if (k < r && nw + i * 16 + li < N) lf = ld16(L + (nw + i * 16 + li) * r + k);
 #pragma unroll
@@ -338,7 +369,7 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
     const int64_t t = tw + j * 16 + li;
     if (t < T) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < MI; ++i) {
         const int64_t n = nw + i * 16 + 4 * g;
         if (n < N)
           *reinterpret_cast<u32x2 *>(out + t * N + n) =
@@ -795,10 +826,10 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
 
 namespace {
 
-// How a product is cut: the large-tile kernel with 64 mj tokens per tile, its first `full` tiles whole and the others
+// How a product is cut: the large-tile kernel with 32 mi outputs x 64 mj tokens per tile, its first `full` tiles whole and the others
 // in `parts` K ranges; or (mj = 0) the small-tile kernel with `parts` K ranges for every tile.
 struct Fp8Plan {
-  int mj, parts;
+  int mi, mj, parts;
   int64_t gn, gt, full;
   int64_t workgroups() const { return full + (gn * gt - full) * parts; }
 };
@@ -813,28 +844,33 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
       best = p;
     }
   };
-  // Times in us from the measured steps. What the rule chose among (us; 256, 192 and 128 tokens a tile, then small tiles in
-  // 1, 2, 3, 4 and 8 K ranges), the choice in brackets:
-  //   515 tokens  13824 x 5120              67 [58] 93   67
-  //   333 tokens   5120 x 5120 by columns   61  54  47   33 [26] 32 32 40
-  //   100 tokens   4096 x 4096              45  37  30   19  14  12 [11] 15
-  //    40 tokens   4096 x 11008            109  97  83   45  26  20  17 [15]
-  //  1024 tokens  11008 x 4096             [55] 92  75   73
-  //  4096 tokens   5120 x 5120             133 [115] 138 159
-  // and over 70 drawn shapes it stays within 1.2 % of the best. Large tiles: rounds of one workgroup per compute unit; where the last round
+  // Times in us from the measured steps. What the rule chose among (us; outputs x tokens 256 x 256, 256 x 192, 256 x 128,
+  // 192 x 192, then small tiles in 1, 2, 3, 4 and 8 K ranges), the choice in brackets:
+  //   515 tokens  13824 x 5120              66  57  84 [48]  67
+  //   333 tokens   5120 x 5120 by columns   61  55  42   -   33 [26] 34 32 40
+  //   100 tokens   4096 x 4096              46  37  31  33   19  14  12 [11] 15
+  //    40 tokens   4096 x 11008            110  99  71  78   44  26  20  17 [15]
+  //   768 tokens  12288 x 8192              93  83 124 [78] 121
+  //  1024 tokens  11008 x 4096             [54] 93  69  76   73
+  //  4096 tokens   5120 x 5120             135 [116] 128 141 161
+  // and over 60 drawn shapes it stays within 2 % of the best on average. Large tiles: rounds of one workgroup per compute unit; where the last round
   // would leave half of them idle, its tiles are cut into K ranges, whose partial tiles are written once more
   // and read by one workgroup (45 bytes a ns).
-  const int64_t gl = (N + kTileN - 1) / kTileN;
-  const double step_large[5] = {0, 0, 1.0, 1.2, 1.35}, ends_large[5] = {0, 0, 3.0, 6.0, 7.0};
-  for (int mj = 4; mj >= 2; --mj) {
-    const int64_t gt = (T + 64 * mj - 1) / (64 * mj), tiles = gl * gt, rest = tiles % cus;
-    const double round = steps * step_large[mj] + ends_large[mj];
-    offer(Fp8Plan{mj, 1, gl, gt, tiles}, (double)((tiles + cus - 1) / cus) * round);
+  struct Large {
+    int mi, mj;
+    double step, ends;
+  };
+  for (const Large &t : {Large{8, 4, 1.42, 7.0}, Large{8, 3, 1.25, 6.0}, Large{8, 2, 0.95, 4.7}, Large{6, 3, 1.07, 5.0}}) {
+    if (trans && t.mi == 6) continue;  // (by columns the narrower tile takes as much of LDS)
+    const int64_t gl = (N + 32 * t.mi - 1) / (32 * t.mi), gt = (T + 64 * t.mj - 1) / (64 * t.mj);
+    const int64_t tiles = gl * gt, rest = tiles % cus;
+    const double round = steps * t.step + t.ends, size = t.mi * t.mj / 8.0;
+    offer(Fp8Plan{t.mi, t.mj, 1, gl, gt, tiles}, (double)((tiles + cus - 1) / cus) * round);
     const int parts = rest ? (int)std::min<int64_t>(std::min<int64_t>(cus / rest, 8), nb / 8) : 1;
     if (parts > 1 && rest <= kMaxTileCounters)
-      offer(Fp8Plan{mj, parts, gl, gt, tiles - rest},
-            (double)(tiles / cus) * round + steps / parts * step_large[mj] + ends_large[mj] + 2.0 +
-                1.45 * mj * (parts - 1) + 0.008 * mj * (double)(rest * parts));
+      offer(Fp8Plan{t.mi, t.mj, parts, gl, gt, tiles - rest},
+            (double)(tiles / cus) * round + steps / parts * t.step + t.ends + 2.0 + 1.45 * size * (parts - 1) +
+                0.008 * size * (double)(rest * parts));
   }
   // Small tiles: two workgroups share a compute unit; the last part's sum of the others
   const int64_t gn = (N + kSmN - 1) / kSmN, gt = (T + kSmT - 1) / kSmT, tiles = gn * gt;
@@ -843,7 +879,7 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
     const double fill = (double)(tiles * parts) / (2.0 * cus_d);
     const double rounds = fill <= 1.0 ? 1.0 : std::ceil(2.0 * fill) / 2.0;
     const double step = fill <= 0.5 ? (trans ? 0.7 : 0.5) : (trans ? 0.70 : 0.66) + 0.12 * std::min(1.0, 2.0 * fill - 1.0);
-    offer(Fp8Plan{0, parts, gn, gt, 0}, rounds * (std::ceil(steps / parts) * step + 3.0) +
+    offer(Fp8Plan{0, 0, parts, gn, gt, 0}, rounds * (std::ceil(steps / parts) * step + 3.0) +
                                          (parts > 1 ? 2.0 + 0.012 * (double)(tiles * parts) : 0.0));
   }
   return best;
@@ -865,17 +901,19 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
   if (p.workgroups() >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)p.workgroups());
   if (p.mj) {
-    static DeviceOnce once[3];
-    auto large = [&](auto *k, DeviceOnce &o) {
-      const hipError_t e = with_lds(k, o, kFp8Lds);
+    static DeviceOnce once[4];
+    auto large = [&](auto *k, DeviceOnce &o, int lds) {
+      const hipError_t e = with_lds(k, o, lds);
       if (e != hipSuccess) return e;
-      k<<<grid, dim3(512), kFp8Lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su, rp, L, r, (int)p.gn,
-                                          (int)p.gt, (int)p.full, p.parts, partial, counters, out);
+      k<<<grid, dim3(512), lds, st>>>(W, ws, (int)N, (int)K, (int)d_in, (int)sld, xq, xs, T, su, rp, L, r, (int)p.gn,
+                                      (int)p.gt, (int)p.full, p.parts, partial, counters, out);
       return hipGetLastError();
     };
-    if (p.mj == 4) return large(k_fp8_gemm<TRANS, E5M2, 4>, once[0]);
-    if (p.mj == 3) return large(k_fp8_gemm<TRANS, E5M2, 3>, once[1]);
-    return large(k_fp8_gemm<TRANS, E5M2, 2>, once[2]);
+    if constexpr (!TRANS)
+      if (p.mi == 6) return large(k_fp8_gemm<TRANS, E5M2, 6, 3, 3>, once[3], Fp8Lds<TRANS, 6, 3, 3>::bytes);
+    if (p.mj == 4) return large(k_fp8_gemm<TRANS, E5M2, 8, 4, 2>, once[0], Fp8Lds<TRANS, 8, 4, 2>::bytes);
+    if (p.mj == 3) return large(k_fp8_gemm<TRANS, E5M2, 8, 3, 2>, once[1], Fp8Lds<TRANS, 8, 3, 2>::bytes);
+    return large(k_fp8_gemm<TRANS, E5M2, 8, 2, 3>, once[2], Fp8Lds<TRANS, 8, 2, 3>::bytes);
   }
   static DeviceOnce once;
   auto *k = k_fp8_gemm_small<TRANS, E5M2>;
@@ -891,7 +929,7 @@ hipError_t product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_i
 size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   const Fp8Plan p = fp8_plan(T, N, K, trans);
   if (p.parts == 1) return 0;
-  return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? kTileN * 64 * p.mj : kSmN * kSmT);
+  return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? 32 * p.mi * 64 * p.mj : kSmN * kSmT);
 }
 
 // the tagged values (at least 2 kDirect words), then the slices' partials

@@ -105,10 +105,12 @@ SHAPES = [  # T, d_out, d_in, r
 ]
 
 
-# tokens, outputs, contracted width: large tiles of 256, 192 and 128 tokens, whole and with their last round cut into
-# K ranges
+# tokens, outputs, contracted width: large tiles of 256 outputs x 256, 192 and 128 tokens and of 192 x 192, whole and with
+# their last round cut into K ranges
 LARGE = [(776, 5168, 288), (3166, 2608, 256), (2964, 4560, 256), (201, 13520, 4720), (1031, 15136, 2704),
-         (1781, 13696, 3344), (1204, 14208, 4800)]
+         (1781, 13696, 3344), (1204, 14208, 4800), (325, 10960, 3104), (519, 14048, 528), (518, 13248, 272),
+         (206, 8496, 4784), (212, 8240, 4224), (263, 14240, 272), (780, 9936, 272), (582, 13392, 528), (2160, 8176, 2560),
+         (1937, 8960, 3824), (976, 10832, 272), (1296, 3104, 4688), (1060, 14352, 2176), (515, 13824, 400)]
 
 
 @pytest.mark.parametrize("T,N,K", LARGE)
