@@ -110,7 +110,8 @@ SHAPES = [  # T, d_out, d_in, r
 LARGE = [(776, 5168, 288), (3166, 2608, 256), (2964, 4560, 256), (201, 13520, 4720), (1031, 15136, 2704),
          (1781, 13696, 3344), (1204, 14208, 4800), (325, 10960, 3104), (519, 14048, 528), (518, 13248, 272),
          (206, 8496, 4784), (212, 8240, 4224), (263, 14240, 272), (780, 9936, 272), (582, 13392, 528), (2160, 8176, 2560),
-         (1937, 8960, 3824), (976, 10832, 272), (1296, 3104, 4688), (1060, 14352, 2176), (515, 13824, 400)]
+         (1937, 8960, 3824), (976, 10832, 272), (1296, 3104, 4688), (1060, 14352, 2176), (515, 13824, 400),
+         (516, 13552, 16), (535, 13344, 144), (198, 16416, 16), (195, 17344, 144), (399, 16496, 16), (581, 16432, 144)]
 
 
 @pytest.mark.parametrize("T,N,K", LARGE)
