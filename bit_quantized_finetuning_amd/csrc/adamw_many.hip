@@ -19,8 +19,8 @@
 // of 256 (4 elements per lane) at a time and a contiguous run of blocks in all;
 // the tensors' addresses travel as a kernel argument, so nothing is copied to
 // the device and a captured launch holds them. Measured: 560 tensors, 250
-// million elements, 8-bit moments, clipped: 1214 us (4.5 TB/s; a large copy
-// reaches 4.7); 14 tensors of one 7B layer, 1.2 million elements: 13.9 us (one
+// million elements, 8-bit moments, clipped: 1198 us (4.6 TB/s; a large copy
+// reaches 4.7); 14 tensors of one 7B layer, 1.2 million elements: 13.5 us (one
 // launch for the norm, one for the step).
 #include "fp8.h"
 #include "host.h"
@@ -31,14 +31,19 @@ namespace qlora {
 constexpr int kManyBlock = 256;
 
 // The job that block b of the launch belongs to (jobs without elements have no
-// blocks): every lane compares two of the jobs' ends, so it takes one load's
-// time (a binary search takes seven, one after another).
-__device__ __forceinline__ int find_job(const ManyJobs &jobs, uint32_t b) {
-  static_assert(kManyJobs <= 128, "two ends per lane");
+// blocks): every lane compares its share of the jobs' ends, so it takes one
+// load's time (a binary search takes seven, one after another).
+template <typename J>
+__device__ __forceinline__ int find_job(const J &jobs, uint32_t b) {
+  constexpr int kMost = sizeof(jobs.blk0) / sizeof(uint32_t) - 1;
   const int lane = threadIdx.x & 63;
-  const uint32_t e0 = lane < jobs.count ? jobs.blk0[lane + 1] : ~0u;
-  const uint32_t e1 = lane + 64 < jobs.count ? jobs.blk0[lane + 65] : ~0u;
-  return __popcll(__ballot(b >= e0)) + __popcll(__ballot(b >= e1));
+  int j = 0;
+#pragma unroll
+  for (int u = 0; u < kMost; u += 64) {
+    const uint32_t end = lane + u < jobs.count ? jobs.blk0[lane + u + 1] : ~0u;
+    j += __popcll(__ballot(b >= end));
+  }
+  return j;
 }
 
 // Four gradients at p, `left` of them inside the tensor.
@@ -73,7 +78,7 @@ __device__ __forceinline__ void load_grad4(const uint16_t *p, int64_t left, floa
 constexpr int kSqAhead = 4;
 
 template <typename G>
-__global__ __launch_bounds__(256) void k_grad_sq(ManyJobs jobs, double *__restrict__ partial) {
+__global__ __launch_bounds__(256) void k_grad_sq(SqJobs jobs, double *__restrict__ partial) {
   __shared__ double red[4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t total = jobs.blk0[jobs.count], nw = gridDim.x * 4;
@@ -85,9 +90,10 @@ __global__ __launch_bounds__(256) void k_grad_sq(ManyJobs jobs, double *__restri
     int j = find_job(jobs, b);
     while (b < end) {
       while (b >= jobs.blk0[j + 1]) ++j;
-      const int64_t first = b - jobs.blk0[j], n = jobs.n[j], e0 = first * kManyBlock + lane * 4;
-      const G *p = static_cast<const G *>(jobs.grad[j]) + e0;
-      if (end - b >= kSqAhead && n / kManyBlock - first >= kSqAhead) {
+      const uint32_t last = jobs.blk0[j + 1] - 1;
+      const int tail = jobs.tail[j];
+      const G *p = static_cast<const G *>(jobs.grad[j]) + (int64_t)(b - jobs.blk0[j]) * kManyBlock + lane * 4;
+      if (end - b >= kSqAhead && last + (tail == kManyBlock) - b >= kSqAhead) {
         float g[kSqAhead][4];
 #pragma unroll
         for (int u = 0; u < kSqAhead; ++u) load_grad4(p + u * kManyBlock, 4, g[u]);
@@ -98,7 +104,7 @@ __global__ __launch_bounds__(256) void k_grad_sq(ManyJobs jobs, double *__restri
         b += kSqAhead;
       } else {
         float g[4];
-        load_grad4(p, n - e0, g);
+        load_grad4(p, b < last ? 4 : tail - lane * 4, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum = fma((double)g[e], (double)g[e], sum);
         ++b;
@@ -236,7 +242,7 @@ __device__ __forceinline__ void step_block(const G *grad, void *param, int64_t l
   for (int e = 0; e < 4; ++e) {
     moments(m[e], v[e], g[e] * coef, a);
     root[e] = sqrtf(v[e]);
-    p[e] = p[e] * a.decay - a.lr * ((m[e] / a.c1) / (root[e] / a.c2 + a.eps));
+    p[e] = p[e] * a.decay - a.lr * ((m[e] * a.c1) / (root[e] * a.c2 + a.eps));
   }
   if (WHOLE) {
     *reinterpret_cast<f32x4 *>(pm) = f32x4{p[0], p[1], p[2], p[3]};
@@ -300,7 +306,8 @@ __device__ __forceinline__ void step_block(const G *grad, void *param, int64_t l
   }
 }
 
-// a.c2 holds sqrt(1 - b2^t) here.
+// a.c1 and a.c2 hold 1 / (1 - b1^t) and 1 / sqrt(1 - b2^t) here (ten instructions less for each division, of 470 a block:
+// 250 million elements 1214 -> 1198 us).
 template <typename G, bool BITS8, bool MASTER>
 __global__ __launch_bounds__(256) void k_adamw_many(ManyJobs jobs, ManyState st, AdamWArgs a, ManyClip clip,
                                                     uint32_t key) {
@@ -342,7 +349,7 @@ static unsigned many_grid(uint32_t blocks) {
   return (unsigned)std::max<int64_t>(1, std::min<int64_t>(cap, (blocks + 3) / 4));
 }
 
-hipError_t launch_grad_sq(const ManyJobs &jobs, bool bf16, double *partial, int *wgs, hipStream_t st) {
+hipError_t launch_grad_sq(const SqJobs &jobs, bool bf16, double *partial, int *wgs, hipStream_t st) {
   const unsigned grid = std::min<unsigned>(many_grid(jobs.blk0[jobs.count]), kManyPartials);
   *wgs = (int)grid;
   if (bf16)

@@ -246,11 +246,10 @@ int qlora_rmsnorm_backward(const void *dy, int64_t ldy, const void *s, int64_t l
 // ---------------------------------------------------------------------------
 // AdamW over many tensors
 // ---------------------------------------------------------------------------
-// The factor, then kManyPartials sums of squares per launch (a tensor without a gradient ends a launch, so there may
-// be one for every other tensor).
+// The factor, then kManyPartials sums of squares per launch of the norm's pass.
 size_t qlora_adamw_many_workspace_bytes(int32_t count) {
   if (count < 0) return 0;
-  return align256(sizeof(float)) + (size_t)std::max<int32_t>(1, count) * kManyPartials * sizeof(double);
+  return align256(sizeof(float)) + (size_t)(count / kSqJobs + 1) * kManyPartials * sizeof(double);
 }
 
 int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlora_adamw_job *jobs, int32_t count,
@@ -293,8 +292,8 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
   a.one_minus_b2 = (float)(1.0 - hp->beta2);
   a.eps = (float)hp->eps;
   a.decay = (float)(1.0 - hp->lr * hp->weight_decay);
-  a.c1 = (float)(1.0 - std::pow(hp->beta1, (double)step));
-  a.c2 = (float)std::sqrt(1.0 - std::pow(hp->beta2, (double)step));
+  a.c1 = (float)(1.0 / (1.0 - std::pow(hp->beta1, (double)step)));
+  a.c2 = (float)(1.0 / std::sqrt(1.0 - std::pow(hp->beta2, (double)step)));
   uint32_t key = seed * 0x9E3779B1u + (uint32_t)step * 0x85157AF5u;
   key ^= key >> 16;
   float *coef = clip ? static_cast<float *>(ws) : nullptr;
@@ -329,11 +328,21 @@ int qlora_adamw_many(const qlora_adamw_many_hparams *hp, int64_t step, const qlo
   if (clip) {
     int n = 0, launches = 0;
     for (int32_t i = 0; i < count;) {
-      i = fill(i);
-      if (t.blk0[t.count] == 0) continue;
+      SqJobs q;
+      q.count = 0;
+      q.blk0[0] = 0;
+      for (; i < count && q.count < kSqJobs; ++i) {
+        if (!jobs[i].grad || jobs[i].n == 0) continue;
+        const int64_t blocks = ceil_div(jobs[i].n, QLORA_ADAMW_BLOCK);
+        q.grad[q.count] = jobs[i].grad;
+        q.tail[q.count] = (uint16_t)(jobs[i].n - (blocks - 1) * QLORA_ADAMW_BLOCK);
+        q.blk0[q.count + 1] = q.blk0[q.count] + (uint32_t)blocks;
+        ++q.count;
+      }
+      if (q.count == 0) continue;
       ++launches;
       int wgs = 0;
-      if (launch_grad_sq(t, grad_dtype == QLORA_BF16, partial + n, &wgs, stream) != hipSuccess) return QLORA_ERR_HIP;
+      if (launch_grad_sq(q, grad_dtype == QLORA_BF16, partial + n, &wgs, stream) != hipSuccess) return QLORA_ERR_HIP;
       n += wgs;
     }
     // One launch's sums are few enough for every workgroup of the step to add itself, which spares a launch (the
