@@ -17,7 +17,8 @@ HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
 SIZES = {
     "edges": [1, 255, 0, 256, 257, 511, 1000, 3],
     "one": [100_003],
-    "many": [64 + 7 * i for i in range(300)],  # three launches
+    "many": [64 + 7 * i for i in range(300)],  # three launches of the step, two of the norm
+    "middle": [100 + 5 * i for i in range(200)],  # two launches and one
     "empty": [0, 0],
     "none": [],
 }
