@@ -8,11 +8,14 @@
 // HBM bounds both: every row is read once and written once, and stays in
 // registers between its reduction and its use (8 values per vector, V vectors
 // per thread, TPR threads per row, chosen from d so that a row just fits). Sums
-// are float32; the row sum is a fixed tree, and dw is summed per workgroup in
+// are float32 (the forward adds its threads' sums in float64, since a root that
+// is off decides scales); the row sum is a fixed tree, and dw is summed per workgroup in
 // registers over its rows, then over workgroups in a fixed order, so results do
 // not depend on scheduling. Measured: 4096 x 8192 with residual, bf16 row and
 // 8-bit row 65 us (4.6 TB/s, a large copy's rate on this card); backward 2047 x
 // 5120 with dw 24 us (3.5 TB/s: 5 of them are dw's second pass).
+#include <cmath>
+
 #include "fp8.h"
 #include "host.h"
 #include "kernels.h"
@@ -93,15 +96,11 @@ __device__ __forceinline__ float as_stored(float v) {
   return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum over the TPR threads of a row (one wave, or a whole workgroup).
+template <int TPR, typename F>
+__device__ __forceinline__ F row_sum(F v, F *red) {
 #pragma unroll
   for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-// Sum over the TPR threads of a row (one wave, or a whole workgroup).
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *red) {
-  v = wave_sum(v);
   if constexpr (TPR > 64) {
     constexpr int NW = TPR / 64;
     __syncthreads();  // the previous row's readers are done
@@ -117,7 +116,7 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 template <typename E, int TPR, int V, bool UNALIGNED>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_fwd(NormFwd a) {
   constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float red[16];
+  __shared__ double red[16];
   const int lt = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
   if (row >= a.T) return;  // whole waves (ROWS > 1 only for one-wave rows)
@@ -143,31 +142,45 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_fwd(NormFwd a
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = fmaf(v[i][e], v[i][e], sum);
   }
-  sum = row_sum<TPR>(sum, red);
-  const float rstd = 1.f / sqrtf(sum / (float)d + a.eps);
+  // the threads' sums are added in float64; the root by one Newton step in it from the float32 one
+  const double x2 = row_sum<TPR>((double)sum, red) / (double)d + (double)a.eps;
+  const double r0 = (double)(1.f / sqrtf((float)x2));
+  const double rd = r0 > 0.0 && r0 < INFINITY ? r0 * (1.5 - 0.5 * x2 * r0 * r0) : r0;
+  const float rstd = (float)rd;
   if (a.rstd && lt == 0) a.rstd[row] = rstd;
   const int ng = (d + kFp8Group - 1) / kFp8Group;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int col = (i * TPR + lt) * 8, left = d - col;
-    float y[8];
+    float y[8], w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd;
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
     if (a.w && left > 0) {
-      float w[8];
       if (a.w_bf16)
         load_vec<UNALIGNED>(static_cast<const uint16_t *>(a.w) + col, left, w);
       else
         load_vec<UNALIGNED>(static_cast<const float *>(a.w) + col, left, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= w[e];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd * w[e];
     if (a.y && left > 0) store_vec<UNALIGNED>(static_cast<E *>(a.y) + row * d + col, left, y);
     if (a.yq) {
       float m = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
       m = max16(m);
+      // Within eight float32 steps of where the scale doubles, the largest value before its roundings decides (v w is
+      // exact in float64), so that they do not cost the group a bit.
+      const uint32_t mb = __float_as_uint(m);
+      if ((mb & 0x7fffffu) - (0x600000u - 8u) < 16u) {
+        double md = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) md = fmax(md, fabs((double)v[i][e] * (double)w[e]) * rd);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) md = fmax(md, __shfl_xor(md, o));
+        const uint32_t edge = (mb & 0xff800000u) | 0x600000u;
+        m = __uint_as_float(edge + (md > (double)__uint_as_float(edge) ? 1u : 0u));
+      }
       const RowScale sc = a.e5m2 ? row_scale<true>(m) : row_scale<false>(m);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] *= sc.inv;

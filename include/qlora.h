@@ -363,7 +363,8 @@ int qlora_fp8_backward(const qlora_fp8_weight *W, const uint16_t *x, const uint1
  *   s = x + residual (rounded to dtype; s = x without one),
  *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight
  * in float32. y is written in dtype, and / or as 8-bit rows (fmt) with scales by
- * qlora_fp8_quantize_rows' rule from the float32 y.
+ * qlora_fp8_quantize_rows' rule from the float32 y (where float32's rounding of
+ * y would decide whether a scale doubles, from y before it).
  *   x, residual  dtype (f32 or bf16) [T, d], rows ldx and ldr elements apart
  *                (>= d), aligned to their element; residual NULL: none
  *   weight       w_dtype (f32 or bf16) [d], NULL: ones

@@ -257,3 +257,26 @@ def test_many_rows_and_far_apart():
     a = q.qlora_rmsnorm_forward(far, None, save_rstd=True)
     b = q.qlora_rmsnorm_forward(far.contiguous(), None, save_rstd=True)
     assert torch.equal(a.y, b.y) and torch.equal(a.rstd, b.rstd)
+
+
+@pytest.mark.parametrize("fmt", [R.E4M3, R.E5M2])
+@pytest.mark.parametrize("d", [4096, 777])
+def test_largest_values_where_the_scale_doubles(d, fmt):
+    """Each group's largest value within a few float32 steps of the format's largest times a power of two: the scale is
+    that of the value before its roundings. (The squares are powers of four, so their float32 sums are exact.)"""
+    say(f"norm edge d={d} {fmt}")
+    g = _gen("edge", d)
+    wrong = 0
+    for T in range(20):
+        x = torch.exp2(torch.randint(-2, 3, (1, d), generator=g, device="cuda").float())
+        rstd = 1 / (x.double().square().mean() + 1e-6).sqrt()
+        w = torch.rand(d, generator=g, device="cuda") * 2.0 ** -6
+        at = torch.arange(0, d, 128, device="cuda") + 5
+        off = 1 + (torch.rand(len(at), generator=g, device="cuda").double() - 0.5) * 2.0 ** -21
+        w[at] = (R.TOP[fmt] * 2.0 ** -9 * off / (x[0, at].double() * rstd)).float()
+        y = x.double() * rstd * w.double()
+        o = q.qlora_rmsnorm_forward(x, w, eps=1e-6, want_y=False, fmt=fmt)
+        assert torch.equal(o.ys.double(), R.row_scales(y, fmt).double())
+        assert torch.isfinite(o.yq.float()).all()
+        wrong += (R.row_scales((x * rstd.float() * w).double(), fmt).double() != o.ys.double()).sum().item()
+    say(f"    scales that float32 alone would have got wrong: {wrong}")
