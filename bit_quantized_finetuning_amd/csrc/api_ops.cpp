@@ -74,6 +74,21 @@ int check_workspace(const void *ws, size_t ws_bytes, size_t need) {
 
 extern "C" {
 
+int qlora_stream_capture_id(uint64_t *id, hipStream_t stream) {
+  if (!id) return QLORA_ERR_NULL;
+  *id = 0;
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  unsigned long long n = 0;
+  const hipError_t e = hipStreamGetCaptureInfo(stream, &status, &n);
+  if (e != hipSuccess) {
+    (void)hipGetLastError();
+    // the null stream while another stream is captured: itself it is not
+    return e == hipErrorStreamCaptureImplicit ? QLORA_OK : QLORA_ERR_HIP;
+  }
+  if (status == hipStreamCaptureStatusActive) *id = (uint64_t)n + 1;
+  return QLORA_OK;
+}
+
 size_t qlora_fp8_storage_bytes(int64_t d_out, int64_t d_in) {
   if (d_out < 1 || d_in < 1) return 0;
   return (size_t)(d_out * d_in + 4 * groups(d_out) * groups(d_in));

@@ -11,7 +11,7 @@ Function names follow the C ABI in include/qlora.h:
     qlora_storage_bytes_absmax,
     qlora_workspace_bytes, qlora_nf4_codebook, qlora_nf4_thresholds, qlora_status_string,
     qlora_fp8_quantize, qlora_fp8_quantize_rows, qlora_fp8_forward, qlora_fp8_backward, qlora_fp8_storage_bytes,
-    qlora_fp8_workspace_bytes, qlora_rmsnorm_forward, qlora_rmsnorm_backward, qlora_adamw_many
+    qlora_fp8_workspace_bytes, qlora_stream_capture_id, qlora_rmsnorm_forward, qlora_rmsnorm_backward, qlora_adamw_many
 
 The C ABI sees only pointers, so every tensor argument is checked here before the call: its shape against the
 weight and the other operands, its dtype, contiguity, and that it lives on the weight's GPU. A mismatch raises
@@ -23,6 +23,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -133,6 +134,7 @@ for _name, _args, _res in (
                                _vp, _vp, _sz, _vp], ctypes.c_int),
         ("qlora_fp8_backward", [ctypes.POINTER(_Fp8Weight), _vp, _vp, ctypes.c_int, _i64, _vp, _vp, _i32, _f32, _vp, _vp,
                                 _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+        ("qlora_stream_capture_id", [ctypes.POINTER(ctypes.c_uint64), _vp], ctypes.c_int),
         ("qlora_rmsnorm_forward", [_vp, _i64, _vp, _i64, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int, _f32, _vp, _vp, _vp,
                                    _vp, ctypes.c_int, _vp, _vp], ctypes.c_int),
         ("qlora_rmsnorm_workspace_bytes", [_i64, _i64], _sz),
@@ -234,33 +236,71 @@ class NF4Weight:
                          torch.empty(ng if double_quant else nb, dtype=torch.float32, device=device))
 
 
-_workspaces: dict = {}
+_workspaces: dict = {}  # (device type, device index, stream) -> workspace
+_captured: dict = {}    # the same key -> (capture, workspace of the calls of that capture)
+# Held from the choice of a shared workspace to the call's last launch: threads that use one stream enqueue whole calls
+# one after another. (Reentrant: an allocation in between may collect garbage.)
+_enqueue = threading.RLock()
+
+
+def _stream_id(dev: torch.device) -> int:
+    """The current stream of a device as an integer (0 for a device without streams)."""
+    return torch.cuda.current_stream(dev).cuda_stream if dev.type == "cuda" else 0
+
+
+def _capture_id(dev: torch.device, stream: int) -> int:
+    """A number for the graph capture that the stream takes part in, 0 when it is not being captured."""
+    if dev.type != "cuda":
+        return 0
+    n = ctypes.c_uint64(0)
+    _check(_lib.qlora_stream_capture_id(ctypes.byref(n), ctypes.c_void_p(stream)), "qlora_stream_capture_id")
+    return int(n.value)
 
 
 def workspace(device, nbytes: int) -> torch.Tensor:
-    """A zero-initialised workspace cached per device (the library leaves its counters zero after each call).
+    """The zero-initialised workspace cached for the device's current stream (the library leaves its counters zero after
+    each call).
 
-    The cached workspace is shared by every call on the device that does not pass its own: calls that may run
-    concurrently (on different streams) must pass distinct workspaces (`ws=`), each zeroed once, e.g. with
+    Every call that does not pass a workspace of its own (`ws=`) uses the cached one of the stream it runs on, so calls
+    on different streams may overlap. Calls captured into a graph share one from the graph's memory pool, cleared by a
+    kernel at its first use in the graph, so that replays share nothing with eager calls or other graphs. A workspace
+    that the caller passes serves one call at a time, in whatever streams; it is zeroed once, e.g. with
     `torch.zeros(qlora_workspace_bytes(...), dtype=torch.uint8, device=...)`.
     """
     dev = torch.device(device)
-    key = (dev.type, dev.index)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        size = max(nbytes, 1 << 20)
-        if ws is not None:
-            size = max(size, 2 * ws.numel())
-        torch.cuda.synchronize(dev)
-        ws = torch.zeros(size, dtype=torch.uint8, device=dev)
-        _workspaces[key] = ws
-    return ws
+    stream = _stream_id(dev)
+    key = (dev.type, dev.index, stream)
+    capture = _capture_id(dev, stream)
+    with _enqueue:
+        if capture:
+            of, ws = _captured.get(key, (0, None))
+            if of != capture or ws.numel() < nbytes:
+                ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
+                ws[:COUNTER_BYTES].zero_()
+                _captured[key] = (capture, ws)
+            return ws
+        ws = _workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            # (allocated on this stream, and replaced in its order: nothing has to be waited for)
+            ws = torch.zeros(max(nbytes, 1 << 20, 0 if ws is None else 2 * ws.numel()), dtype=torch.uint8, device=dev)
+            _workspaces[key] = ws
+        return ws
 
 
 def _own_workspace(ws: torch.Tensor, nbytes: int) -> torch.Tensor:
     if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < nbytes:
         raise ValueError(f"ws must be a contiguous uint8 tensor of at least {nbytes} bytes")
     return ws
+
+
+@contextlib.contextmanager
+def _ws_for(ws, dev, nbytes: int):
+    """The caller's workspace, or the stream's cached one for as long as the call enqueues its launches."""
+    if ws is not None:
+        yield _own_workspace(ws, nbytes)
+        return
+    with _enqueue:
+        yield workspace(dev, nbytes)
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -508,11 +548,10 @@ def qlora_forward(w: NF4Weight, x: torch.Tensor, A: torch.Tensor | None, B: torc
     h and u may be passed in (preallocated outputs); otherwise they are allocated here.
     """
     T, r, h, u = _forward_args(w, x, A, B, h, u, save_u, ws)
-    if ws is None:
-        ws = workspace(x.device, qlora_workspace_bytes(w.d_out, w.d_in, T, r))
     cw = w._c()
-    _check(_lib.qlora_forward(ctypes.byref(cw), _ptr(x), T, _ptr(A), _ptr(B), r, alpha, _ptr(h), _ptr(u),
-                              _ptr(ws), ws.numel(), _stream(x.device)), "qlora_forward")
+    with _ws_for(ws, x.device, qlora_workspace_bytes(w.d_out, w.d_in, T, r)) as ws:
+        _check(_lib.qlora_forward(ctypes.byref(cw), _ptr(x), T, _ptr(A), _ptr(B), r, alpha, _ptr(h), _ptr(u),
+                                  _ptr(ws), ws.numel(), _stream(x.device)), "qlora_forward")
     return h, u
 
 
@@ -572,17 +611,15 @@ def qlora_forward_many(jobs, ws: torch.Tensor | None = None):
         outs.append((h, u))
     _check_independent(args)
     nbytes = qlora_forward_many_workspace_bytes(len(jobs))
-    if ws is None:
-        ws = workspace(dev, nbytes)
-    else:
-        _own_workspace(ws, nbytes)
+    if ws is not None:
         _check_devices(dev, ws=ws)
     cws = [a[0]._c() for a in args]  # kept alive for the call
     arr = (_ForwardJob * len(args))()
     for k, (a, cw) in enumerate(zip(args, cws)):
         w, x, T, A, B, r, alpha, h, u = a
         arr[k] = _ForwardJob(ctypes.pointer(cw), _ptr(x), T, _ptr(A), _ptr(B), r, alpha, _ptr(h), _ptr(u))
-    _check(_lib.qlora_forward_many(arr, len(args), _ptr(ws), ws.numel(), _stream(dev)), "qlora_forward_many")
+    with _ws_for(ws, dev, nbytes) as ws:
+        _check(_lib.qlora_forward_many(arr, len(args), _ptr(ws), ws.numel(), _stream(dev)), "qlora_forward_many")
     return outs
 
 
@@ -658,10 +695,10 @@ def qlora_backward(w: NF4Weight, x: torch.Tensor | None, dY: torch.Tensor, A: to
         dA = torch.empty(r, w.d_in, dtype=torch.float32, device=dev)
     if dB is None and need_dB and r > 0:
         dB = torch.empty(w.d_out, r, dtype=torch.float32, device=dev)
-    ws = workspace(dev, nbytes) if ws is None else ws
     cw = w._c()
-    _check(_lib.qlora_backward(ctypes.byref(cw), _ptr(x), _ptr(dY), T, _ptr(A), _ptr(B), r, alpha, _ptr(u_saved),
-                               _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(dev)), "qlora_backward")
+    with _ws_for(ws, dev, nbytes) as ws:
+        _check(_lib.qlora_backward(ctypes.byref(cw), _ptr(x), _ptr(dY), T, _ptr(A), _ptr(B), r, alpha, _ptr(u_saved),
+                                   _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(dev)), "qlora_backward")
     return dX, dA, dB
 
 
@@ -705,28 +742,14 @@ def _done(answer, where: str):
     return answer
 
 
-def _cached_ws(dev: int):
-    """The device's cached workspace for a native call (None while a graph is captured, see _call_ws)."""
-    return None if torch.cuda.is_current_stream_capturing() else _workspaces.get(("cuda", dev))
+def _cached_ws(dev: int, stream: int):
+    """The stream's cached workspace for a native call (None while a graph is captured, see workspace)."""
+    return None if torch.cuda.is_current_stream_capturing() else _workspaces.get(("cuda", dev, stream))
 
 
 def _on(dev):
     """The library launches on the current device: make `dev` current where it is not."""
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-def _call_ws(dev, nbytes: int, ws, counters: bool = True):
-    """The caller's workspace, or the device's cached one. A call that is being captured into a graph gets one of
-    its own from the graph's memory pool (with its counters cleared by a kernel of the graph), so that replays
-    share nothing with eager calls or other graphs."""
-    if ws is not None:
-        return _own_workspace(ws, nbytes)
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        if counters:
-            ws[:COUNTER_BYTES].zero_()
-        return ws
-    return workspace(dev, nbytes)
 
 
 @dataclass
@@ -817,8 +840,10 @@ def qlora_fp8_forward(w: Fp8Weight, x: torch.Tensor | None, A: torch.Tensor | No
     f = _fmt(fmt)
     if h is None and u is None and ws is None and w.codes.is_cuda:
         dev = torch.cuda.current_device()
-        out = _marshal.fp8_forward(w.codes, w.scales, w.d_out, w.d_in, x, A, B, alpha, xq, xs, f, save_u,
-                                   _cached_ws(dev), dev, _raw_stream(dev))
+        stream = _raw_stream(dev)
+        with _enqueue:
+            out = _marshal.fp8_forward(w.codes, w.scales, w.d_out, w.d_in, x, A, B, alpha, xq, xs, f, save_u,
+                                       _cached_ws(dev, stream), dev, stream)
         if out is not None:
             return _done(out, "qlora_fp8_forward")
     _check_fp8_weight(w)
@@ -853,8 +878,7 @@ def qlora_fp8_forward(w: Fp8Weight, x: torch.Tensor | None, A: torch.Tensor | No
     if u is None and save_u and r > 0:
         u = torch.empty(T, r, dtype=torch.float32, device=dev)
     cw = w._c()
-    with _on(dev):
-        ws = _call_ws(dev, nbytes, ws)
+    with _on(dev), _ws_for(ws, dev, nbytes) as ws:
         _check(_lib.qlora_fp8_forward(ctypes.byref(cw), _ptr(xq), _ptr(xs), f, _ptr(x), T, _ptr(A), _ptr(B), r, alpha,
                                       _ptr(h), _ptr(u), _ptr(ws), ws.numel(), _stream(dev)), "qlora_fp8_forward")
     return h, u
@@ -869,8 +893,10 @@ def qlora_fp8_backward(w: Fp8Weight, x: torch.Tensor | None, dY: torch.Tensor, A
     f = _fmt(fmt)
     if dX is None and dA is None and dB is None and ws is None and w.codes.is_cuda:
         dev = torch.cuda.current_device()
-        out = _marshal.fp8_backward(w.codes, w.scales, w.d_out, w.d_in, x, dY, A, B, alpha, u_saved, need_dx, need_dA,
-                                    need_dB, f, _cached_ws(dev), dev, _raw_stream(dev))
+        stream = _raw_stream(dev)
+        with _enqueue:
+            out = _marshal.fp8_backward(w.codes, w.scales, w.d_out, w.d_in, x, dY, A, B, alpha, u_saved, need_dx, need_dA,
+                                        need_dB, f, _cached_ws(dev, stream), dev, stream)
         if out is not None:
             return _done(out, "qlora_fp8_backward")
     _check_fp8_weight(w)
@@ -902,8 +928,7 @@ def qlora_fp8_backward(w: Fp8Weight, x: torch.Tensor | None, dY: torch.Tensor, A
     if dB is None and need_dB:
         dB = torch.empty(w.d_out, r, dtype=torch.float32, device=dev)
     cw = w._c()
-    with _on(dev):
-        ws = _call_ws(dev, nbytes, ws)
+    with _on(dev), _ws_for(ws, dev, nbytes) as ws:
         _check(_lib.qlora_fp8_backward(ctypes.byref(cw), _ptr(x), _ptr(dY), f, T, _ptr(A), _ptr(B), r, alpha,
                                        _ptr(u_saved), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(dev)),
                "qlora_fp8_backward")

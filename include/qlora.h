@@ -174,7 +174,10 @@ int qlora_merge(const qlora_nf4_weight *W, const uint16_t *A, const uint16_t *B,
  *          must be zero before the first use of the workspace; every call leaves
  *          them zero again, except the last one, which counts the waits that ran
  *          out of time (qlora_workspace_fallbacks; the output never depends on
- *          it). The rest of the workspace needs no initialisation.
+ *          it). The rest of the workspace needs no initialisation. A workspace
+ *          serves one call at a time: calls that may overlap (on different
+ *          streams, or a graph's replay beside other work) and calls that
+ *          different threads enqueue take workspaces of their own
  * T <= 16 runs one weight-streaming kernel (the adapter intermediate is formed
  * by the last workgroups of the same launch); larger T runs the MFMA GEMM.
  */
@@ -305,6 +308,13 @@ typedef struct {
   uint8_t *codes;
   float *scales;
 } qlora_fp8_weight;
+
+/*
+ * *id: a number for the graph capture that the stream takes part in (another for every capture), 0 when the stream is
+ * not being captured; for callers that keep a workspace per stream and give captured calls one of their own.
+ * Errors: NULL, HIP.
+ */
+int qlora_stream_capture_id(uint64_t *id, hipStream_t stream);
 
 /* Bytes of an 8-bit weight: n + 4 * ceil(d_out / 128) * ceil(d_in / 128). */
 size_t qlora_fp8_storage_bytes(int64_t d_out, int64_t d_in);
