@@ -7,8 +7,10 @@
 // it is scaled in float32 and added to the running float32 sum, so nothing is
 // rounded below 32 bits before the one rounding to bf16. The weight is the first
 // operand: a lane then holds one token (one xs) and four consecutive outputs.
+#include <atomic>
 #include <cmath>
 
+#include "exchange.h"
 #include "fp8.h"
 #include "host.h"
 #include "kernels.h"
@@ -582,12 +584,10 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 // The adapter's u = x A^T [T, r] is formed by the first workgroups of the same
 // launch (one per 16 ranks and slice of K; the last of the slices to arrive adds
 // them in order) while the others stream, and reaches them as 64-bit words: one
-// bf16(s u), 16 fixed bits that no finite float32 or bf16 left in the workspace
-// by an earlier call can hold there, and the launch's tag. A reader whose wait
-// runs out (other launches hold the compute units) forms what it misses itself,
-// in the same order of operations, so no wait needs another workgroup to run and
-// the result
-// does not depend on who formed what. Where the slices' partials are at most one
+// bf16(s u) and 48 bits that only this launch has (exchange.h). A reader whose
+// wait runs out (other launches hold the compute units) forms what it misses
+// itself, in the same order of operations, so no wait needs another workgroup to
+// run and the result does not depend on who formed what. Where the slices' partials are at most one
 // per thread of a reader (one token up to rank 64 of 4096 x 8192, four up to 16),
 // every reader takes and adds those instead, which spares the hop through the
 // last slice (1 token, 4096 x 4096: rank 16 8.6 -> 7.4 us, rank 64 9.3 -> 8.3). One compute unit reads about 28 GB/s from
@@ -606,15 +606,11 @@ struct StreamAdapter {
   float scale;
   float *u_out;
   bool direct;     // readers add the slices' partials themselves
-  uint64_t *ex;    // [T][rp] tagged values; direct: [slices][T][rp][2] tagged halves of float32 partials
+  uint64_t mark;   // of this launch's words (exchange.h)
+  uint64_t *ex;    // [T][rp] values as words; direct: [slices][T][rp][2] halves of float32 partials
   float *partial;  // [rp / 16][slices][4][64] quarters
   uint32_t *counters;
 };
-
-// A value in the exchange: bf16 bits, a pattern that is NaN as the upper half of a float32 and as a bf16, the launch.
-__device__ __forceinline__ uint64_t tagged(uint32_t bits, uint32_t tag) {
-  return (uint64_t)tag << 32 | 0xffa50000u | (bits & 0xffffu);
-}
 
 // Slice ks of K of u for ranks 16 rt .. +15, all tokens: lane l of wave 0 gets token l & 15, ranks 16 rt + 4 (l >> 4) + i.
 __device__ __forceinline__ f32x4 u_partial(const StreamAdapter &a, int K, int T, int rt, int ks, f32x4 (*red)[64]) {
@@ -658,7 +654,6 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
   __shared__ uint32_t missing[QLORA_MAX_RANK / 16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, g = lane >> 4;
-  const uint32_t tag = producers ? launch_tag() : 0u;
   if ((int)blockIdx.x < producers) {
     const int rt = blockIdx.x / ad.slices, ks = blockIdx.x - rt * ad.slices;
     f32x4 u = u_partial(ad, K, T, rt, ks, red);
@@ -669,8 +664,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
       for (int i = 0; i < 4; ++i) {
         const uint32_t bits = __float_as_uint(u[i]);
         if (li < T) {
-          st_dev_u64(to + 2 * i, tagged(bits, tag));
-          st_dev_u64(to + 2 * i + 1, tagged(bits >> 16, tag));
+          st_dev_u64(to + 2 * i, exchange_word(ad.mark, bits));
+          st_dev_u64(to + 2 * i + 1, exchange_word(ad.mark, bits >> 16));
         }
       }
       return;
@@ -699,7 +694,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
       const int j = 16 * rt + 4 * g;
       uint64_t *to = ad.ex + li * ad.rp + j;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st_dev_u64(to + i, tagged(pack_bf16x2(u[i] * ad.scale, 0.f), tag));
+      for (int i = 0; i < 4; ++i) st_dev_u64(to + i, exchange_word(ad.mark, pack_bf16x2(u[i] * ad.scale, 0.f)));
       if (ad.u_out && j < ad.r) *reinterpret_cast<f32x4 *>(ad.u_out + li * ad.r + j) = u;
     }
     return;
@@ -744,7 +739,6 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
   if (producers) {
     constexpr int kAll = 64 * kStreamWaves, kPoll = 4;  // words of a thread asked for at once
     const int tiles = ad.rp / 16, values = T * ad.rp;
-    const uint64_t mark = tagged(0u, tag) >> 16;
     if (tid < tiles) missing[tid] = 0u;
     __syncthreads();
     const long long t0 = wall_clock64(), limit = wait_limit(ad.counters + kMaxCounters - 1);
@@ -752,7 +746,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
       float *const part = reinterpret_cast<float *>(red);
       while (tid < values * ad.slices) {
         const uint64_t lo = ld_dev_u64(ad.ex + 2 * tid), hi = ld_dev_u64(ad.ex + 2 * tid + 1);
-        if ((lo >> 16) == mark && (hi >> 16) == mark) {
+        if (exchange_holds(lo, ad.mark) && exchange_holds(hi, ad.mark)) {
           part[tid] = __uint_as_float((uint32_t)hi << 16 | ((uint32_t)lo & 0xffffu));
           break;
         }
@@ -776,16 +770,16 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
         uint64_t v[kPoll];
         bool all = true;
 #pragma unroll
-        for (int u = 0; u < kPoll; ++u) v[u] = e0 + u * kAll < values ? ld_dev_u64(ad.ex + e0 + u * kAll) : mark << 16;
+        for (int u = 0; u < kPoll; ++u) v[u] = e0 + u * kAll < values ? ld_dev_u64(ad.ex + e0 + u * kAll) : ad.mark;
 #pragma unroll
-        for (int u = 0; u < kPoll; ++u) all = all && (v[u] >> 16) == mark;
+        for (int u = 0; u < kPoll; ++u) all = all && exchange_holds(v[u], ad.mark);
         const bool late = !all && wall_clock64() - t0 > limit;
         if (all || late) {
 #pragma unroll
           for (int u = 0; u < kPoll; ++u) {
             const int e = e0 + u * kAll, t = e / ad.rp, j = e - t * ad.rp;
             if (e >= values) continue;
-            if ((v[u] >> 16) == mark)
+            if (exchange_holds(v[u], ad.mark))
               su[t * kSuPitch + j] = (uint16_t)v[u];
             else
               missing[j / 16] = 1u;
@@ -822,6 +816,11 @@ __global__ __launch_bounds__(64 * kStreamWaves) void k_fp8_stream(const uint8_t 
     *reinterpret_cast<u32x2 *>(out + (int64_t)li * N + n0 + 4 * g) =
         u32x2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
   }
+}
+
+__global__ __launch_bounds__(256) void k_clear_words(uint64_t *__restrict__ p, int n) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0u;
 }
 
 namespace {
@@ -932,7 +931,7 @@ size_t fp8_partial_floats(int64_t T, int64_t N, int64_t K, bool trans) {
   return (size_t)((p.gn * p.gt - p.full) * p.parts) * (p.mj ? 32 * p.mi * 64 * p.mj : kSmN * kSmT);
 }
 
-// the tagged values (at least 2 kDirect words), then the slices' partials
+// the words of the exchange (at least 2 kDirect), then the slices' partials
 namespace {
 size_t exchange_words(int rp) { return (size_t)std::max(16 * rp, 2 * kDirect); }
 }  // namespace
@@ -942,8 +941,22 @@ hipError_t launch_fp8_stream(const uint8_t *W, const float *ws, int64_t N, int64
                              bool e5m2, int64_t T, const uint16_t *x, const uint16_t *A, const uint16_t *B, int r, int rp,
                              float scale, float *u_out, void *ex, uint32_t *counters, uint16_t *out,
                              hipStream_t st) {
+  static std::atomic<uint64_t> launches{0};
   const int slices = (int)std::min<int64_t>(kUSlices, (K + 1023) / 1024);
-  const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, T * rp * slices <= kDirect, static_cast<uint64_t *>(ex),
+  const bool direct = T * rp * slices <= kDirect;
+  if (r > 0) {
+    // (a query that fails is of a stream that the launches below fail on too)
+    hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(st, &capture) != hipSuccess) (void)hipGetLastError();
+    if (capture != hipStreamCaptureStatusNone) {
+      const int words = (int)T * rp * (direct ? 2 * slices : 1);
+      k_clear_words<<<dim3((unsigned)((words + 255) / 256)), dim3(256), 0, st>>>(static_cast<uint64_t *>(ex), words);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  const StreamAdapter ad{x, A, B, r, rp, slices, scale, u_out, direct, exchange_mark(launches.fetch_add(1)),
+                         static_cast<uint64_t *>(ex),
                          reinterpret_cast<float *>(static_cast<uint64_t *>(ex) + exchange_words(rp)), counters};
   const int producers = r > 0 ? rp / 16 * slices : 0;
   const dim3 grid((unsigned)(N / 16 + producers)), block(64 * kStreamWaves);

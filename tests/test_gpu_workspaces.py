@@ -153,3 +153,54 @@ def test_graphs_replayed_beside_each_other(base):
         torch.cuda.synchronize()
         for i, w in enumerate(want):
             assert _same(outs[0][i], w) and _same(outs[1][len(calls) - 1 - i], w) and _same(eager[i], w), (k, i)
+
+
+@pytest.mark.parametrize("T,r", [(1, 16), (16, 64), (5, 256)])
+def test_one_workspace_on_two_streams_in_turn(T, r):
+    """The adapter's x A^T travels between workgroups in the workspace: calls on two streams, ordered by events, that
+    find the other stream's values there, each with new inputs."""
+    say(f"fp8 one workspace, two streams in turn T={T} r={r}")
+    N, K = 1024, 2064
+    g = _gen("turns", T, r)
+    w = q.qlora_fp8_quantize(_randn(g, N, K) * 0.02)
+    A, B = (_randn(g, r, K) * 0.02).bfloat16(), (_randn(g, N, r) * 0.02).bfloat16()
+    xs = [_randn(g, T, K).bfloat16() for _ in range(40)]
+    fresh = lambda: torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, r), dtype=torch.uint8, device="cuda")  # noqa: E731
+    want = [q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True, ws=fresh()) for x in xs]
+    ws = fresh()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for k, x in enumerate(xs):
+        st = streams[k % 2]
+        st.wait_stream(streams[(k + 1) % 2])
+        with torch.cuda.stream(st):
+            got.append(q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True, ws=ws))
+    torch.cuda.synchronize()
+    for k, (a, b) in enumerate(zip(got, want)):
+        assert _same(a, b), k
+
+
+@pytest.mark.parametrize("T,r", [(1, 16), (16, 64)])
+def test_captured_call_with_a_given_workspace(T, r):
+    """A replay finds the values of the replay before it in the workspace: it takes its own."""
+    say(f"fp8 captured call, given workspace T={T} r={r}")
+    N, K = 1024, 2064
+    g = _gen("replay", T, r)
+    w = q.qlora_fp8_quantize(_randn(g, N, K) * 0.02)
+    A, B = (_randn(g, r, K) * 0.02).bfloat16(), (_randn(g, N, r) * 0.02).bfloat16()
+    x = _randn(g, T, K).bfloat16()
+    ws = torch.zeros(q.qlora_fp8_workspace_bytes(N, K, T, r), dtype=torch.uint8, device="cuda")
+    q.qlora_fp8_forward(w, x, A, B, 16.0, ws=ws)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True, ws=ws)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(12):
+        x.copy_(_randn(g, T, K))
+        want = q.qlora_fp8_forward(w, x, A, B, 16.0, save_u=True)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[k % 2]):
+            gr.replay()
+        torch.cuda.synchronize()
+        assert _same(out, want), k

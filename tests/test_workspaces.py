@@ -2,6 +2,7 @@
 threads that share a stream one after another. (The buffers are host memory here; streams and captures are numbers.)"""
 
 import os
+import subprocess
 import threading
 import time
 
@@ -91,3 +92,14 @@ def test_a_given_workspace_is_the_callers(now):
 
 def test_capture_number_refuses():
     assert q.lib.qlora_stream_capture_id(None, None) == -1
+
+
+def test_marks_of_the_exchange(tmp_path):
+    """What a single-token launch's workgroups hand each other carries a mark that no other launch has, whatever its
+    stream or queue."""
+    root = _build.ROOT
+    exe = tmp_path / "exchange_check"
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-I", _build.CSRC, os.path.join(root, "tests", "c_abi", "exchange_check.cpp"),
+                    "-o", str(exe)], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0 and run.stdout == "shared marks 0\nfinite 0 lost 0 zero 0\n", run.stdout
