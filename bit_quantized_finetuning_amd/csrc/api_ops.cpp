@@ -45,7 +45,7 @@ Fp8Layout fp8_layout(int64_t d_out, int64_t d_in, int64_t T, int r) {
     return at;
   };
   L.ex = take(T <= kFp8StreamTokens ? fp8_stream_exchange_bytes(rp) : 0);
-  L.su = take((size_t)std::max<int64_t>(16, ceil_div(T, 16) * 16) * rp * 2);
+  L.su = take((size_t)T * rp * 2 * 2);  // two bf16 terms
   L.u = take((size_t)T * r * 4);
   L.v = take((size_t)T * r * 4);
   L.lt = take((size_t)r * d_in * 2);

@@ -8,6 +8,8 @@
 // scale first.
 #pragma once
 
+#include <cmath>
+
 #include "common.h"
 
 namespace qlora {
@@ -66,6 +68,17 @@ __device__ __forceinline__ float max16(float v) {
 template <bool B_E5M2>
 __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, B_E5M2 ? 1 : 0, 0, 0, 0, 0);
+}
+
+// Two float32 values as two bf16 terms each: the upper 8 bits of the significand
+// (cut, so that nothing rounds up to an infinity) and the rest, rounded: at most
+// 2^-15 of the value is lost. An infinity leaves no rest.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  auto rest = [](float x) {
+    return fabsf(x) == INFINITY ? 0.f : x - __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  };
+  hi = perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  lo = pack_bf16x2(rest(a), rest(b));
 }
 
 __device__ __forceinline__ i32x8 join8(u32x4 lo, u32x4 hi) {

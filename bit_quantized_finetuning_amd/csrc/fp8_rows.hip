@@ -211,9 +211,18 @@ __global__ __launch_bounds__(64 * NW) void k_fp8_rows(RowsJob a, int rp, int ksp
     if (t >= T) return;
     const bool real = j < a.r;  // r % 8 == 0: four ranks are in or out together
     if (a.out_f32 && real) *reinterpret_cast<f32x4 *>(a.out_f32 + t * a.r + j) = v;
-    if (a.out_bf16 && j < rp)
-      *reinterpret_cast<u32x2 *>(a.out_bf16 + t * rp + j) =
-          real ? u32x2{pack_bf16x2(a.scale * v[0], a.scale * v[1]), pack_bf16x2(a.scale * v[2], a.scale * v[3])} : u32x2{0, 0};
+    if (a.out_terms && j < rp) {
+      u32x2 hi = {0, 0}, lo = {0, 0};
+      if (real) {
+        uint32_t h0, l0, h1, l1;
+        split_bf16x2(a.scale * v[0], a.scale * v[1], h0, l0);
+        split_bf16x2(a.scale * v[2], a.scale * v[3], h1, l1);
+        hi = u32x2{h0, h1};
+        lo = u32x2{l0, l1};
+      }
+      *reinterpret_cast<u32x2 *>(a.out_terms + t * rp + j) = hi;
+      *reinterpret_cast<u32x2 *>(a.out_terms + (T + t) * rp + j) = lo;
+    }
   };
   if (ksplit == 1) {
 #pragma unroll

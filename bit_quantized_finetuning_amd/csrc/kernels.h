@@ -199,8 +199,8 @@ hipError_t launch_adapter_grad(const AdapterGradJob &a, const AdapterGradJob &b,
 size_t adapter_grad_partial_floats(int64_t Da, int64_t Db, int R, int64_t T);
 
 // fp8_rows.hip: one pass over bf16 rows P [T, K] (K % 16 == 0): their 8-bit codes and scales (codes == NULL: not), and
-// out[T, r] = P Q^T with Q = A [r, K] or, q_is_b, B [K, r] (r % 8 == 0, r > 0): out_f32 [T, r] (nullable), out_bf16 =
-// bf16(scale out) [T, rp] (nullable, zero columns r .. rp - 1); and lt [d_lt, r] = A^T for A [r, d_lt] (lt == NULL: not).
+// out[T, r] = P Q^T with Q = A [r, K] or, q_is_b, B [K, r] (r % 8 == 0, r > 0): out_f32 [T, r] (nullable), out_terms [2]
+// [T, rp] = scale out as two bf16 terms (nullable, zero columns r .. rp - 1); and lt [d_lt, r] = A^T for A [r, d_lt] (lt == NULL: not).
 // Uses `partial` (fp8_rows_partial_floats) and `counters` (one tile_counter per 64 tokens or fewer).
 struct RowsJob {
   const uint16_t *P;
@@ -211,7 +211,7 @@ struct RowsJob {
   int r;
   float scale;
   float *out_f32;
-  uint16_t *out_bf16;
+  uint16_t *out_terms;
   const uint16_t *A;
   uint16_t *lt;
   int64_t d_lt;
@@ -229,8 +229,8 @@ hipError_t launch_fp8_quantize_weight(const void *W, bool bf16_in, int64_t N, in
                                       hipStream_t st);
 
 // fp8_gemm.hip: out[T, N] = the block-scaled product of xq [T, K] with the e4m3 weight [d_out, d_in] (trans false:
-// N = d_out, K = d_in; true: the weight read by columns, N = d_in, K = d_out) + su L^T (su bf16 [T, rp], L bf16
-// [N, r]; r may be 0). Uses `partial` (fp8_partial_floats) and `counters` (one tile_counter per output tile).
+// N = d_out, K = d_in; true: the weight read by columns, N = d_in, K = d_out) + su L^T (su [2][T, rp]: the
+// sum of two bf16 terms; L bf16 [N, r]; r may be 0). Uses `partial` (fp8_partial_floats) and `counters` (one tile_counter per output tile).
 hipError_t launch_fp8_product(const uint8_t *W, const float *ws, int64_t d_out, int64_t d_in, bool trans,
                               const uint8_t *xq, const float *xs, bool e5m2, int64_t T, const uint16_t *su, int rp,
                               const uint16_t *L, int r, uint16_t *out, float *partial, uint32_t *counters,
