@@ -34,12 +34,13 @@ __device__ __forceinline__ int rw_row(int s) { return (s & 3) | ((s >> 3) & 7) <
 // half of the LDS cycles were conflicts).
 __device__ __forceinline__ int rw_turn(int row) { return (row + 4) & 15; }
 
-// Stores issued from asm. (No write of their data registers follows within the wait state they need.)
+// Stores issued from asm. The registers of a store of more than 8 bytes may not be written in the next two wait states;
+// the compiler keeps that distance for stores it knows, here the s_nop behind the store does, whatever comes next.
 __device__ __forceinline__ void store16_asm(const i32x4 &rs, const u32x4 &v, uint32_t off) {
-  asm volatile("buffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 0" : : "v"(v), "v"(off), "s"(rs) : "memory");
+  asm volatile("buffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" : : "v"(v), "v"(off), "s"(rs) : "memory");
 }
 __device__ __forceinline__ void store4_asm(const i32x4 &rs, uint32_t v, uint32_t off) {
-  asm volatile("buffer_store_dword %0, %1, %2, 0 offen\n\ts_nop 0" : : "v"(v), "v"(off), "s"(rs) : "memory");
+  asm volatile("buffer_store_dword %0, %1, %2, 0 offen" : : "v"(v), "v"(off), "s"(rs) : "memory");
 }
 
 // FMT: 0 no codes, 1 e4m3, 2 e5m2. BT: Q is B [K, r].
