@@ -277,8 +277,9 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
   need(m.defined() && v.defined() && seed >= 0 && seed < ((int64_t)1 << 32));
   need(max_norm > 0.f || as_float(a[13]) == 0.0);  // (0: no clipping; what float32 turns into 0 is refused)
   std::vector<qlora_adamw_job> jobs((size_t)count);
-  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans, reads;  // what is written; the gradients
   spans.reserve((size_t)count + 6);
+  reads.reserve((size_t)count);
   int gd = -1, pd = -1;
   int64_t total = 0;
   for (Py_ssize_t i = 0; i < count; ++i) {
@@ -294,6 +295,10 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
       const int gt = float_type(g);
       if (gd < 0) gd = gt;
       need(gt == gd && g.numel() == size && g.is_contiguous());
+      if (size) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(g.data_ptr());
+        reads.emplace_back(at, at + (uintptr_t)size * g.element_size());
+      }
     }
     on(dev, {&g, &p});
     jobs[(size_t)i] = qlora_adamw_job{ptr(g), p.data_ptr(), size};
@@ -310,6 +315,10 @@ PyObject *adamw_many(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
   std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i) need(spans[i - 1].second <= spans[i].first);
+  for (const auto &g : reads) {  // (gradients may overlap each other)
+    const auto next = std::lower_bound(spans.begin(), spans.end(), std::make_pair(g.second, (uintptr_t)0));
+    need(next == spans.begin() || (next - 1)->second <= g.first);
+  }
   if (gd < 0) gd = QLORA_F32;
   const bool bits8 = m.scalar_type() == at::kFloat8_e4m3fn;
   need(bits8 || m.scalar_type() == at::kFloat);

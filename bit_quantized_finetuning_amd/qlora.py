@@ -20,6 +20,7 @@ TypeError (dtype) or ValueError (shape, layout, device) and nothing is launched.
 
 from __future__ import annotations
 
+import bisect
 import contextlib
 import ctypes
 import os
@@ -1064,6 +1065,12 @@ def _neighbours(spans):
     return zip(spans, spans[1:])
 
 
+def _meets(span, spans) -> bool:
+    """Whether a span overlaps one of `spans` (sorted, none overlapping another)."""
+    i = bisect.bisect_left(spans, (span[1],))  # the first that starts at or past its end
+    return i > 0 and spans[i - 1][1] > span[0]
+
+
 def adamw_state_elements(sizes) -> int:
     """Elements of the flat state of tensors of these sizes: each starts at a multiple of 256."""
     return sum(-(-n // ADAMW_BLOCK) * ADAMW_BLOCK for n in sizes)
@@ -1133,11 +1140,15 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     if not 0 <= int(seed) < 1 << 32:
         raise ValueError("seed must fit in 32 bits")
     _arg(norm, "norm", torch.float32, (1,))
-    for t in (m, v, m_scale, v_scale, master, norm):
+    if ws is not None and max_norm is not None:
+        _own_workspace(ws, int(_lib.qlora_adamw_many_workspace_bytes(count)))
+    for t in (m, v, m_scale, v_scale, master, norm, ws if max_norm is not None else None):
         if t is not None and t.numel():
-            spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+            spans.append(_span(t))
     if any(a[1] > b[0] for a, b in _neighbours(spans)):
-        raise ValueError("the state, the parameters and norm must not overlap")
+        raise ValueError("the state, the parameters, norm and workspace must not overlap")
+    if any(_meets(_span(g), spans) for g in grads if g is not None and g.numel()):
+        raise ValueError("a gradient overlaps a parameter, the state, norm or the workspace")
     if max_norm is None and norm is not None:
         raise ValueError("norm is given but max_norm is not")
     if max_norm is not None and not ctypes.c_float(max_norm).value > 0:

@@ -429,7 +429,8 @@ size_t qlora_rmsnorm_workspace_bytes(int64_t T, int64_t d);
  *   seed     8-bit moments are rounded stochastically, by bits that depend on
  *            (seed, step, the element's place): the same call gives the same bits
  *   ws       qlora_adamw_many_workspace_bytes(count) bytes (no initialisation)
- * All device memory, 16-byte aligned. n < 2^38, fewer than 2^31 blocks in all.
+ * All device memory, 16-byte aligned. n < 2^38, fewer than 2^31 blocks in all. No parameter, state array, norm or ws
+ * may overlap another or a gradient (gradients may overlap each other).
  * Errors: NULL, SHAPE, DTYPE, VALUE, ALIGN, WORKSPACE, HIP.
  */
 typedef struct {
