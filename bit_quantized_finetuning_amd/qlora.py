@@ -3,7 +3,8 @@
 Argument marshalling only: every step of the layer runs in the HIP library.
 PyTorch supplies device memory and the current HIP stream; the library itself
 allocates nothing. If the library is missing this module raises at import --
-there is no fallback path.
+there is no fallback path. (_marshal.so, the same marshalling in C++ for the
+calls made most often, may be missing: those calls then take longer on the host.)
 
 Function names follow the C ABI in include/qlora.h:
     qlora_quantize, qlora_dequantize, qlora_merge, qlora_forward, qlora_forward_noalloc, qlora_backward,
@@ -25,6 +26,7 @@ import contextlib
 import ctypes
 import os
 import threading
+import warnings
 from dataclasses import dataclass
 from typing import NamedTuple
 
@@ -51,9 +53,10 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 try:
     from . import _marshal  # native marshalling of the calls made most often (csrc/binding.cpp)
-except ImportError as e:
-    raise ImportError(f"{os.path.dirname(LIB_PATH)}/_marshal.so is not built ({e}); run "
-                      "`python -m bit_quantized_finetuning_amd.build`") from e
+except ImportError as e:  # not built, or against another torch: every call has its Python marshalling too
+    _marshal = None
+    warnings.warn(f"{os.path.dirname(LIB_PATH)}/_marshal.so does not load ({e}): calls are marshalled in Python, which "
+                  "takes a few times as long per call; run `python -m bit_quantized_finetuning_amd.build`", RuntimeWarning)
 
 
 class _Nf4Weight(ctypes.Structure):
@@ -839,7 +842,7 @@ def qlora_fp8_forward(w: Fp8Weight, x: torch.Tensor | None, A: torch.Tensor | No
     quantized to fmt within the call. x itself is needed then, and for the adapter. u is float32 [T, r] when
     save_u or given, else None."""
     f = _fmt(fmt)
-    if h is None and u is None and ws is None and w.codes.is_cuda:
+    if _marshal is not None and h is None and u is None and ws is None and w.codes.is_cuda:
         dev = torch.cuda.current_device()
         stream = _raw_stream(dev)
         with _enqueue:
@@ -892,7 +895,7 @@ def qlora_fp8_backward(w: Fp8Weight, x: torch.Tensor | None, dY: torch.Tensor, A
     """Returns (dX bf16 [T, d_in] | None, dA f32 [r, d_in] | None, dB f32 [d_out, r] | None); dY is quantized to fmt
     within the call for dX's product with the base, and used as it is for the adapter."""
     f = _fmt(fmt)
-    if dX is None and dA is None and dB is None and ws is None and w.codes.is_cuda:
+    if _marshal is not None and dX is None and dA is None and dB is None and ws is None and w.codes.is_cuda:
         dev = torch.cuda.current_device()
         stream = _raw_stream(dev)
         with _enqueue:
@@ -980,7 +983,7 @@ def qlora_rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, r
     (float32 or bfloat16, any row stride). y comes in x's dtype (want_y) and / or as 8-bit rows with scales (fmt:
     torch.float8_e4m3fn or torch.float8_e5m2), as qlora_fp8_forward takes them."""
     f = 0 if fmt is None else _fmt(fmt)
-    if torch.is_tensor(x) and x.is_cuda:
+    if _marshal is not None and torch.is_tensor(x) and x.is_cuda:
         dev = torch.cuda.current_device()
         out = _marshal.rmsnorm_forward(x, weight, residual, eps, want_y, f, save_rstd, dev, _raw_stream(dev))
         if out is not None:
@@ -1016,7 +1019,7 @@ def qlora_rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tens
                            ds: torch.Tensor | None = None, need_dw: bool = False, ws: torch.Tensor | None = None):
     """Returns (dx, dw): dx in s's dtype is the gradient of x and of the residual; dw float32 [d] when need_dw. dy is
     the gradient of y, ds the one that reaches s past the norm (both in s's dtype, any row stride)."""
-    if ws is None and torch.is_tensor(s) and s.is_cuda:
+    if _marshal is not None and ws is None and torch.is_tensor(s) and s.is_cuda:
         dev = torch.cuda.current_device()
         out = _marshal.rmsnorm_backward(dy, s, weight, rstd, ds, need_dw, dev, _raw_stream(dev))
         if out is not None:
@@ -1090,7 +1093,8 @@ def qlora_adamw_many(step: int, grads, params, m: torch.Tensor, v: torch.Tensor,
     bits that depend on (seed, step, place) alone. max_norm: gradients are scaled to at most that global norm first,
     and a norm that is not finite leaves everything as it was; the norm is returned (float32 [1], on the device)."""
     grads, params = list(grads), list(params)
-    if ws is None and (max_norm is None or max_norm > 0) and torch.is_tensor(m) and m.is_cuda:
+    if (_marshal is not None and ws is None and (max_norm is None or max_norm > 0) and torch.is_tensor(m)
+            and m.is_cuda):
         dev = torch.cuda.current_device()
         out = _marshal.adamw_many(step, grads, params, m, v, m_scale, v_scale, master, lr, beta1, beta2, eps,
                                   weight_decay, 0.0 if max_norm is None else max_norm, seed, norm, dev, _raw_stream(dev))
