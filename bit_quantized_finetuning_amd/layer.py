@@ -22,7 +22,8 @@ The frozen base can also be kept in 8-bit floating point (base="fp8": e4m3 with 
 qlora_fp8_quantize): the forward multiplies 8-bit rows of the input with it, the backward 8-bit rows of the upstream
 gradient (the adapter's products stay in bf16). The input's 8-bit rows come from the norm before the projection
 (QLoRARMSNorm writes them beside its bf16 rows) or are formed within the call; gradients pass straight through that
-rounding.
+rounding. grad_fmt is the 8-bit format of the upstream gradient's rows: torch.float8_e4m3fn (the default, three bits of
+mantissa) or torch.float8_e5m2 (two, and a range of 2^32 within a group instead of 2^18).
 
 A training step of these modules can be captured into a graph once nothing keeps an earlier eager step's outputs or
 loss: torch ties a leaf's gradient accumulation to the stream of the graph that lives, and a backward that is captured
@@ -138,6 +139,7 @@ class _Bf16Module(torch.nn.Module):
     """Dtype casts leave the quantized storage and the bf16 adapters as they are; device moves apply."""
 
     base = "nf4"  # of modules that do not say (a subclass's, or saved before there was a choice)
+    grad_fmt = q.E4M3
 
     def _apply(self, fn, recurse=True):
         def keep_dtype(t):
@@ -146,10 +148,15 @@ class _Bf16Module(torch.nn.Module):
 
         return super()._apply(keep_dtype, recurse)
 
-    def _register_base(self, weight: torch.Tensor, base: str, double_quant: bool):
+    def _register_base(self, weight: torch.Tensor, base: str, double_quant: bool, grad_fmt):
         """Quantize the frozen weight (base "nf4" or "fp8") into buffers: frozen state, not parameters."""
         if base not in ("nf4", "fp8"):
             raise ValueError(f"base must be 'nf4' or 'fp8', got {base!r}")
+        if grad_fmt is not None:
+            q._fmt(grad_fmt)
+            if base != "fp8":
+                raise ValueError("grad_fmt is for a base in 8-bit floating point")
+            self.grad_fmt = grad_fmt
         self.base = base
         if base == "fp8":
             w = q.qlora_fp8_quantize(weight)
@@ -173,7 +180,7 @@ class _Bf16Module(torch.nn.Module):
     def _project(self, x2, A, B, alpha, recompute_u, sink, xq, xs):
         """One call over the base; xq, xs: the 8-bit rows of x2 (8-bit base only)."""
         if self.base == "fp8":
-            return Fp8LinearFunction.apply(x2, A, B, self.w, alpha, recompute_u, sink, xq, xs)
+            return Fp8LinearFunction.apply(x2, A, B, self.w, alpha, recompute_u, sink, xq, xs, self.grad_fmt)
         if xq is not None or xs is not None:
             raise ValueError("8-bit rows are for a base in 8-bit floating point")
         return QLoRALinearFunction.apply(x2, A, B, self.w, alpha, recompute_u, sink)
@@ -189,12 +196,12 @@ class QLoRALinear(_Bf16Module):
 
     def __init__(self, weight: torch.Tensor, r: int = 8, alpha: float = 16.0, freeze_A: bool = False,
                  generator: torch.Generator | None = None, double_quant: bool = True, recompute_u: bool = False,
-                 base: str = "nf4"):
+                 base: str = "nf4", grad_fmt=None):
         super().__init__()
         if weight.dim() != 2:
             raise ValueError("weight must be [d_out, d_in]")
         d_out, d_in = weight.shape
-        self._register_base(weight.contiguous(), base, double_quant)
+        self._register_base(weight.contiguous(), base, double_quant, grad_fmt)
         self.d_out, self.d_in, self.r, self.alpha = d_out, d_in, r, float(alpha)
         self.d_w_out = d_out
         self.recompute_u = recompute_u
@@ -244,7 +251,7 @@ class QLoRAFusedLinear(_Bf16Module):
     """
 
     def __init__(self, weights, r: int = 8, alpha: float = 16.0, adapted=None, double_quant: bool = True,
-                 generator: torch.Generator | None = None, base: str = "nf4"):
+                 generator: torch.Generator | None = None, base: str = "nf4", grad_fmt=None):
         super().__init__()
         weights = [w.contiguous() for w in weights]
         d_in = weights[0].shape[1]
@@ -258,7 +265,7 @@ class QLoRAFusedLinear(_Bf16Module):
         n_ad = sum(self.adapted) if r > 0 else 0
         if n_ad * r > q.MAX_RANK:
             raise ValueError(f"{n_ad} adapters of rank {r} exceed the library's rank limit {q.MAX_RANK}")
-        self._register_base(torch.cat(weights, 0), base, double_quant)
+        self._register_base(torch.cat(weights, 0), base, double_quant, grad_fmt)
         self.d_w_out = sum(self.d_outs)
         self.A = torch.nn.ParameterList()
         self.B = torch.nn.ParameterList()

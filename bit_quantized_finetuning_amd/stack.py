@@ -17,7 +17,7 @@ With checkpoint=True each layer keeps only its input and runs its forward again 
 
 base="fp8" keeps the projections' frozen weights in 8-bit floating point instead: the norms are then the library's
 (QLoRARMSNorm), which write the 8-bit rows that q/k/v and gate/up multiply, and the one before the MLP adds the
-residual in the same pass.
+residual in the same pass. grad_fmt is then the 8-bit format of the projections' upstream gradients.
 
 Weights come from the seeded device generator of the synthetic-input module, one seed per layer, so that a
 layer's weights can be drawn again to check it.
@@ -46,17 +46,17 @@ class DecoderProjections(torch.nn.Module):
     bf16 [d_out, d_in] tensors."""
 
     def __init__(self, weights: dict, r: int = 8, alpha: float = 16.0, generator: torch.Generator | None = None,
-                 head: int = HEAD, base: str = "nf4"):
+                 head: int = HEAD, base: str = "nf4", grad_fmt=None):
         super().__init__()
         self.base = base
         self.hidden, self.kv, self.head = weights["q"].shape[0], weights["k"].shape[0], head
         if self.hidden % head or self.kv % head or self.hidden % self.kv:
             raise ValueError("q and k/v widths must be multiples of the head width, q's of k's")
         self.qkv = QLoRAFusedLinear([weights["q"], weights["k"], weights["v"]], r=r, alpha=alpha,
-                                    adapted=[True, False, True], generator=generator, base=base)
-        self.o = QLoRALinear(weights["o"], r=0, base=base)
-        self.gate_up = QLoRAFusedLinear([weights["gate"], weights["up"]], r=0, base=base)
-        self.down = QLoRALinear(weights["down"], r=0, base=base)
+                                    adapted=[True, False, True], generator=generator, base=base, grad_fmt=grad_fmt)
+        self.o = QLoRALinear(weights["o"], r=0, base=base, grad_fmt=grad_fmt)
+        self.gate_up = QLoRAFusedLinear([weights["gate"], weights["up"]], r=0, base=base, grad_fmt=grad_fmt)
+        self.down = QLoRALinear(weights["down"], r=0, base=base, grad_fmt=grad_fmt)
         self.norm = QLoRARMSNorm(self.hidden, fmt=q_.E4M3) if base == "fp8" else None
 
     def _heads(self, t: torch.Tensor, rep: int) -> torch.Tensor:
@@ -91,7 +91,8 @@ class DecoderStack(torch.nn.Module):
     to the 14B-style layer) and its adapters' A are drawn from synth.stack_adapter_init(i) (B starts at zero)."""
 
     def __init__(self, layers: int = 40, shapes: dict | None = None, r: int = 8, alpha: float = 16.0,
-                 seed: int = 0, device="cuda", checkpoint: bool = True, head: int = HEAD, base: str = "nf4"):
+                 seed: int = 0, device="cuda", checkpoint: bool = True, head: int = HEAD, base: str = "nf4",
+                 grad_fmt=None):
         super().__init__()
         self.shapes = dict(synth.STACK_SHAPES if shapes is None else shapes)
         self.seed = seed
@@ -100,7 +101,8 @@ class DecoderStack(torch.nn.Module):
         for i in range(layers):
             ws = synth.stack_layer_weights(i, device, self.shapes, seed)
             gen = synth.stack_adapter_init(i, device, seed)
-            self.layers.append(DecoderProjections(ws, r=r, alpha=alpha, generator=gen, head=head, base=base))
+            self.layers.append(DecoderProjections(ws, r=r, alpha=alpha, generator=gen, head=head, base=base,
+                                                  grad_fmt=grad_fmt))
             del ws
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:

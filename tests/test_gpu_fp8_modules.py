@@ -1,0 +1,67 @@
+"""Gradients of the modules over the 8-bit base (needs an MI355X), in both formats of the upstream gradient."""
+
+import zlib
+
+import pytest
+import torch
+
+import ops_ref as R
+from gpu_common import product, say
+
+q = product("qlora")
+layer = product("layer")
+stack = product("stack")
+
+
+def _gen(*key):
+    return torch.Generator(device="cuda").manual_seed(zlib.crc32(repr(key).encode()))
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [None, R.E4M3, R.E5M2])
+def test_format_of_the_upstream_gradient(fmt):
+    say(f"fp8 modules, upstream gradient in {fmt}")
+    g = _gen("fmt")
+    W = _randn(g, 384, 400) * 0.02
+    x, dh = _randn(g, 37, 400).bfloat16(), _randn(g, 37, 384).bfloat16()
+    lin = layer.QLoRALinear(W, r=16, base="fp8", generator=_gen("a"), grad_fmt=fmt)
+    fused = layer.QLoRAFusedLinear([W[:128], W[128:]], r=8, adapted=[True, False], base="fp8", generator=_gen("b"), grad_fmt=fmt)
+    with torch.no_grad():
+        lin.B.copy_(_randn(g, 384, 16) * 0.02)
+        fused.B[0].copy_(_randn(g, 128, 8) * 0.02)
+    for m, A, B in ((lin, lin.A, lin.B), (fused, *fused.stacked_adapter())):
+        xg = x.clone().requires_grad_(True)
+        h = m(xg)
+        (torch.cat(h, 1) if isinstance(h, tuple) else h).backward(dh)
+        outs = {f: q.qlora_fp8_backward(m.w, x, dh, A.detach(), B.detach(), 16.0, fmt=f)[0] for f in (R.E4M3, R.E5M2)}
+        assert not torch.equal(outs[R.E4M3], outs[R.E5M2])
+        assert torch.equal(xg.grad, outs[fmt or R.E4M3])
+
+
+@pytest.mark.gpu
+def test_stack_passes_the_format_on():
+    say("fp8 stack, upstream gradients in e5m2")
+    shapes = {"q": (256, 256), "k": (128, 256), "v": (128, 256), "o": (256, 256), "gate": (384, 256), "up": (384, 256), "down": (256, 384)}
+    grads = []
+    for fmt in (None, R.E4M3, R.E5M2):
+        st = stack.DecoderStack(layers=2, shapes=shapes, r=8, seed=5, device=torch.device("cuda:0"), head=64, base="fp8", grad_fmt=fmt)
+        for lay in st.layers:
+            assert all(m.grad_fmt is (fmt or R.E4M3) for m in (lay.qkv, lay.o, lay.gate_up, lay.down))
+        x = _randn(_gen("x"), 45, 256).bfloat16().requires_grad_(True)
+        st(x).backward(_randn(_gen("dy"), 45, 256).bfloat16())
+        grads.append(x.grad)
+    assert torch.equal(grads[0], grads[1]) and not torch.equal(grads[0], grads[2])
+    assert torch.isfinite(grads[2]).all()
+
+
+def test_format_is_for_the_eight_bit_base():
+    W = torch.zeros(64, 64)
+    for make in (lambda **k: layer.QLoRALinear(W, **k), lambda **k: layer.QLoRAFusedLinear([W], **k)):
+        with pytest.raises(ValueError, match="grad_fmt"):
+            make(base="nf4", grad_fmt=R.E5M2)
+        with pytest.raises(TypeError, match="float8"):
+            make(base="fp8", grad_fmt=torch.bfloat16)
