@@ -87,7 +87,14 @@ double as_float(PyObject *o) {
   }
   return v;
 }
-bool as_bool(PyObject *o) { return PyObject_IsTrue(o) == 1; }
+bool as_bool(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    throw Refused{};
+  }
+  return v == 1;
+}
 hipStream_t as_stream(PyObject *o) { return reinterpret_cast<hipStream_t>(as_int(o)); }
 
 PyObject *results(std::initializer_list<Tensor> ts) {
