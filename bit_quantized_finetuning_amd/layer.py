@@ -330,10 +330,16 @@ class QLoRARMSNorm(torch.nn.Module):
         self.dim, self.eps, self.fmt = int(dim), float(eps), fmt
         self.weight = None if weight is None else torch.nn.Parameter(weight.detach().clone(), requires_grad=trainable)
 
+    def _rows(self, t: torch.Tensor) -> torch.Tensor:
+        """t as rows that the call takes: dense ones that do not overlap (a broadcast or transposed input is copied)."""
+        t = t.reshape(-1, self.dim)
+        dense = (self.dim == 1 or t.stride(1) == 1) and (t.shape[0] <= 1 or t.stride(0) >= self.dim)
+        return t if dense else t.contiguous()
+
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None):
         """(y, s, yq, ys): y and s = x + residual in x's shape (s is x without a residual), yq [tokens, dim] and ys the
         8-bit rows and scales (None without fmt)."""
-        x2 = x.reshape(-1, self.dim)
-        r2 = None if residual is None else residual.reshape(-1, self.dim)
+        x2 = self._rows(x)
+        r2 = None if residual is None else self._rows(residual)
         y, s, yq, ys = RMSNormFunction.apply(x2, self.weight, r2, self.eps, self.fmt)
         return y.reshape(x.shape), x if s is None else s.reshape(x.shape), yq, ys

@@ -65,3 +65,27 @@ def test_format_is_for_the_eight_bit_base():
             make(base="nf4", grad_fmt=R.E5M2)
         with pytest.raises(TypeError, match="float8"):
             make(base="fp8", grad_fmt=torch.bfloat16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_of_broadcast_and_transposed_inputs(dtype):
+    """Rows that overlap or are not dense, as the projections' modules take them: values and gradients of the dense copy."""
+    say(f"norm module, broadcast and transposed inputs {dtype}")
+    g = _gen("broadcast")
+    n = layer.QLoRARMSNorm(64, weight=1 + 0.1 * _randn(g, 64), trainable=True, fmt=R.E4M3)
+    row, wide, deep = _randn(g, 1, 1, 64).to(dtype), _randn(g, 64, 5).to(dtype), _randn(g, 3, 64, 5).to(dtype)
+    views = ((row, lambda t: t.expand(3, 5, 64)), (wide, lambda t: t.t()), (wide, lambda t: t.t()[::2]),
+             (deep, lambda t: t.transpose(1, 2)))
+    for src, make in views:
+        shape = make(src).shape
+        for res in (None, _randn(g, 64).to(dtype).expand(shape)):
+            a, b = src.clone().requires_grad_(True), src.clone().requires_grad_(True)
+            dy = _randn(g, *shape).to(dtype)
+            got = n(make(a), res)
+            want = n(make(b).contiguous(), None if res is None else res.contiguous())
+            for s, t in zip(got, want):
+                assert torch.equal(s, t)
+            got[0].backward(dy)
+            want[0].backward(dy)
+            assert torch.equal(a.grad, b.grad)
