@@ -45,6 +45,8 @@ class DecoderProjections(torch.nn.Module):
     """One decoder layer of projections (see the module docstring); `weights` maps q, k, v, o, gate, up, down to
     bf16 [d_out, d_in] tensors."""
 
+    base = "nf4"  # of layers saved before there was a choice
+
     def __init__(self, weights: dict, r: int = 8, alpha: float = 16.0, generator: torch.Generator | None = None,
                  head: int = HEAD, base: str = "nf4", grad_fmt=None):
         super().__init__()
