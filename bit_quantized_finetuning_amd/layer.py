@@ -25,6 +25,9 @@ gradient (the adapter's products stay in bf16). The input's 8-bit rows come from
 rounding. grad_fmt is the 8-bit format of the upstream gradient's rows: torch.float8_e4m3fn (the default, three bits of
 mantissa) or torch.float8_e5m2 (two, and a range of 2^32 within a group instead of 2^18).
 
+Gradients of gradients are refused over the 8-bit base and through the norm (their backward is the library's, which
+autograd cannot look into).
+
 A training step of these modules can be captured into a graph once nothing keeps an earlier eager step's outputs or
 loss: torch ties a leaf's gradient accumulation to the stream of the graph that lives, and a backward that is captured
 on another stream while an eager one lives ends the process.
@@ -72,6 +75,29 @@ class QLoRALinearFunction(torch.autograd.Function):
                 None)
 
 
+class _Opaque(torch.autograd.Function):
+    """`n` results of the library and the tensors that they were formed from -> the results, as functions of those tensors
+    whose derivative is refused."""
+
+    @staticmethod
+    def forward(ctx, n: int, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("gradients of gradients: the library's backward cannot be differentiated")
+
+
+def _once(results, *formed_from):
+    """Results of a backward. Where autograd records the backward itself (create_graph), a derivative that would leave out
+    what lies inside the library raises."""
+    if not torch.is_grad_enabled():
+        return results
+    given = [t for t in results if t is not None]
+    opaque = iter(_Opaque.apply(len(given), *given, *(t for t in formed_from if t is not None)) if given else ())
+    return tuple(None if t is None else next(opaque) for t in results)
+
+
 class Fp8LinearFunction(torch.autograd.Function):
     """As QLoRALinearFunction over an 8-bit base; xq, xs: x's 8-bit rows and scales, or None."""
 
@@ -95,8 +121,8 @@ class Fp8LinearFunction(torch.autograd.Function):
                                           need_dB=ctx.r > 0 and ctx.needs_input_grad[2], fmt=ctx.grad_fmt)
         if ctx.grad_sink is not None:
             ctx.grad_sink(dA, dB)
-        return (dX, None if dA is None else dA.to(A.dtype), None if dB is None else dB.to(B.dtype), None, None, None,
-                None, None, None, None)
+        grads = dX, None if dA is None else dA.to(A.dtype), None if dB is None else dB.to(B.dtype)
+        return *_once(grads, dh, x, A, B), None, None, None, None, None, None, None
 
 
 class RMSNormFunction(torch.autograd.Function):
@@ -123,7 +149,8 @@ class RMSNormFunction(torch.autograd.Function):
         else:
             dx, dw = q.qlora_rmsnorm_backward(dy.contiguous(), s, weight, rstd, ds=None if ds is None else ds.contiguous(),
                                               need_dw=need_dw)
-        return dx, None if dw is None else dw.to(weight.dtype), dx if ctx.has_residual else None, None, None
+            dx, dw = _once((dx, None if dw is None else dw.to(weight.dtype)), dy, ds, s, weight)
+        return dx, dw, dx if ctx.has_residual else None, None, None
 
 
 def _deposit_fp32(p: torch.nn.Parameter, g: torch.Tensor):

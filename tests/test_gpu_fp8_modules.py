@@ -89,3 +89,26 @@ def test_norm_of_broadcast_and_transposed_inputs(dtype):
             got[0].backward(dy)
             want[0].backward(dy)
             assert torch.equal(a.grad, b.grad)
+
+
+@pytest.mark.gpu
+def test_gradients_of_gradients_are_refused():
+    """The library's backward is not differentiable: a second derivative raises instead of leaving its terms out."""
+    say("fp8 modules, second derivatives")
+    g = _gen("twice")
+    n = layer.QLoRARMSNorm(64, weight=1 + 0.1 * _randn(g, 64))
+    lin = layer.QLoRALinear(_randn(g, 64, 64) * 0.02, r=8, base="fp8", generator=g)
+    for f in (lambda x: n(x)[0], lin):
+        x = _randn(g, 5, 64).bfloat16().requires_grad_(True)
+        a = _randn(g, 5, 64).bfloat16().requires_grad_(True)
+        # d/dx of a sum over f(x a): a times what the library gives, which itself depends on a
+        (dx,) = torch.autograd.grad(f(x * a).float().square().sum(), x, create_graph=True)
+        for second in (lambda: torch.autograd.grad(dx.float().square().sum(), a, retain_graph=True), lambda: dx.float().sum().backward()):
+            with pytest.raises(RuntimeError, match="gradients of gradients"):
+                second()
+        a.grad = x.grad = None
+        f(x * a).sum().backward(create_graph=True)  # once it is
+        first = x.grad.detach().clone()
+        x.grad = None
+        f(x * a).sum().backward()
+        assert torch.isfinite(first).all() and torch.equal(first, x.grad)
