@@ -112,3 +112,123 @@ def test_gradients_of_gradients_are_refused():
         x.grad = None
         f(x * a).sum().backward()
         assert torch.isfinite(first).all() and torch.equal(first, x.grad)
+
+
+def _check(name, got, ref, bound):
+    worst = ((got.double() - ref).abs() / bound.clamp_min(1e-300)).max().item()
+    say(f"    {name}: largest error / bound = {worst:.3f}")
+    assert got.shape == ref.shape and worst <= 1.0, f"{name}: {worst} times the bound"
+
+
+def _projection_gradients(x, dY, w, fmt, adapters=(), s=0.0):
+    """dX of a projection over the base w from the upstream gradient that it got, and dA, dB of its adapters (first output
+    row, A, B): (value, bound) each, in 64 bits.
+
+    dX: the base's product of dY's 8-bit rows (R.product_bound), and each adapter's s (dY B) A with v = dY B off by a
+    float32 step per term and 2^-15 left out of s v by its two bf16 terms. dA, dB: float32 operands with all their bits,
+    float32 sums over the tokens."""
+    T, N = dY.shape
+    codes, scales = R.quantize_rows(dY, fmt)
+    yh, wh = codes * R.spread_cols(scales, N), R.restored_weight(w.codes, w.scales).t()
+    ref, extra, grads = yh @ wh.t(), 0.0, []
+    X, lim = x.double(), (T + 8) * 2.0 ** -23
+    for row, A, B in adapters:
+        Ad, Bd, D = A.detach().double(), B.detach().double(), dY[:, row:row + B.shape[0]].double()
+        v, vb = D @ Bd, (N + 4) * 2.0 ** -23 * (D.abs() @ Bd.abs())
+        U, ub = X @ Ad.t(), (X.shape[1] + 4) * 2.0 ** -23 * (X.abs() @ Ad.abs().t())
+        ref = ref + s * v @ Ad
+        lost = 2.0 ** -15 + (2 * 256 + 8) * 2.0 ** -23
+        extra = extra + s * (lost * v.abs() + (1 + lost) * vb) @ Ad.abs()
+        grads.append(((s * v.t() @ X, s * (lim * v.abs().t() + vb.t()) @ X.abs()),
+                      (s * D.t() @ U, s * D.abs().t() @ (lim * U.abs() + ub))))
+    return (ref, R.product_bound(yh, wh, ref, extra)), grads
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [R.E4M3, R.E5M2])
+@pytest.mark.parametrize("T", [5, 37, 300])
+def test_gradients_of_fused_projections(T, fmt):
+    """Against the formulas in 64 bits, each projection's adapter from its own rows of the stacked gradient."""
+    say(f"fp8 fused gradients T={T} {fmt}")
+    g = _gen("fused", T)
+    outs = (256, 144, 128)
+    f = layer.QLoRAFusedLinear([_randn(g, n, 400) * 0.02 for n in outs], r=24, alpha=32.0, adapted=[True, False, True], base="fp8",
+                               generator=g, grad_fmt=fmt)
+    with torch.no_grad():
+        for B in f.B:
+            B.copy_(_randn(g, *B.shape) * 0.05)
+    x = _randn(g, T, 400).bfloat16().requires_grad_(True)
+    dY = (_randn(g, T, sum(outs)) * torch.exp2(_randn(g, T, 1))).bfloat16()
+    torch.cat(f(x), 1).backward(dY)
+    (dX, bound), grads = _projection_gradients(x.detach(), dY, f.w, fmt, [(0, f.A[0], f.B[0]), (400, f.A[1], f.B[1])], 32.0 / 24)
+    _check("dX", x.grad, dX, bound)
+    for k, (a, b) in enumerate(grads):
+        _check(f"dA {k}", f.A[k].grad_fp32, *a)
+        _check(f"dB {k}", f.B[k].grad_fp32, *b)
+        assert torch.equal(f.A[k].grad, f.A[k].grad_fp32.bfloat16()) and torch.equal(f.B[k].grad, f.B[k].grad_fp32.bfloat16())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", [R.E4M3, R.E5M2])
+def test_gradients_inside_the_stack(fmt):
+    """Every projection and norm of every layer: its gradients against the 64-bit formulas, from the inputs and the upstream
+    gradient that it really got."""
+    say(f"fp8 stack gradients {fmt}")
+    shapes = {"q": (256, 256), "k": (128, 256), "v": (128, 256), "o": (256, 256), "gate": (384, 256), "up": (384, 256), "down": (256, 384)}
+    st = stack.DecoderStack(layers=3, shapes=shapes, r=8, seed=5, device=torch.device("cuda:0"), checkpoint=False, head=64, base="fp8",
+                            grad_fmt=fmt)
+    g = _gen("inside")
+    seen = []
+
+    def note(module, args, out):
+        ins = [t for t in args if torch.is_tensor(t) and t.requires_grad]
+        outs = [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None and t.requires_grad]
+        for t in (*ins, *outs):
+            if not t.is_leaf:
+                t.retain_grad()
+        seen.append((module, args, ins, out, outs))
+
+    with torch.no_grad():
+        for lay in st.layers:
+            for B in lay.qkv.B:
+                B.copy_(_randn(g, *B.shape) * 0.05)
+    for lay in st.layers:
+        for m in (lay.qkv, lay.o, lay.gate_up, lay.down, lay.norm):
+            m.register_forward_hook(note)
+        lay.norm.register_forward_hook(lambda m, a, k, o: seen.append((m, a + (k["residual"],), None, o, None)) if k else None,
+                                       with_kwargs=True)
+    x = _randn(g, 45, 256).bfloat16().requires_grad_(True)
+    st(x).backward(_randn(g, 45, 256).bfloat16())
+    checked = 0
+    for module, args, ins, out, outs in seen:
+        if outs is None or isinstance(module, layer.QLoRARMSNorm):
+            continue
+        dY = torch.cat([t.grad for t in outs], 1)
+        adapters = []
+        if isinstance(module, layer.QLoRAFusedLinear) and len(module.A):
+            adapters = [(0, module.A[0], module.B[0]), (module.d_outs[0] + module.d_outs[1], module.A[1], module.B[1])]
+        (dX, bound), grads = _projection_gradients(args[0].detach(), dY, module.w, fmt, adapters, 16.0 / 8)
+        assert len(ins) == 1 and ins[0] is args[0]
+        _check(f"dX of {tuple(module.codes.shape)}", ins[0].grad, dX, bound)
+        for k, (a, b) in enumerate(grads):
+            _check(f"dA {k}", module.A[k].grad_fp32, *a)
+            _check(f"dB {k}", module.B[k].grad_fp32, *b)
+        checked += 1
+    assert checked == 12
+    # the norms before the MLPs: dx + ds of the sum, from y's and s's own gradients (the residual's reaches the same sum)
+    norms = 0
+    for module, args, _, out, outs in seen:
+        if not isinstance(module, layer.QLoRARMSNorm) or outs is not None or len(args) < 2:
+            continue
+        y, s = out[0], out[1]
+        sd = s.detach().double().requires_grad_(True)
+        yd = sd * torch.rsqrt(sd.square().mean(-1, keepdim=True) + 1e-6)
+        dy, ds = y.grad.double(), s.grad.double()
+        ref = torch.autograd.grad((yd * dy).sum(), sd)[0] + ds
+        # float32 sums of 256 terms of size |dy xh| rstd, then one rounding to bf16
+        rstd = torch.rsqrt(sd.detach().square().mean(-1, keepdim=True) + 1e-6)
+        xh = (sd.detach() * rstd).abs()
+        acc = (256 + 16) * 2.0 ** -23 * (rstd * (dy.abs() + xh * (dy.abs() * xh).mean(-1, keepdim=True)) + ds.abs())
+        _check("dx of the norm", args[0].grad, ref, 2.0 ** -8 * (ref.abs() + acc) + acc)
+        norms += 1
+    assert norms == 3
