@@ -28,13 +28,13 @@ namespace qlora {
 // Both operands' tiles go from memory straight into LDS (S tiles of each, steps
 // k + 1 .. k + S - 1 on their way during step k), as do the token scales.
 // 256 outputs x 256 tokens for whole batches, and 256 x 192, 192 x 192 (by rows)
-// or 256 x 128 where that leaves fewer compute units idle. With all of them at
-// work on 256 x 256 two stages keep up with the clock that power allows; the
-// smaller tiles' steps last as long as the copies take, so those that have room
-// for three stages have them (515 tokens, 13824 x 5120: 192 x 192 54 -> 48 us,
-// 256 x 128 92 -> 84). Measured:
-// 4096 tokens, 22016 x 8192: 641 us (2300 TFLOP/s) by rows, 633 by columns; the
-// matrix unit is busy half of the cycles, at the clock that power leaves it.
+// or 256 x 128 where that leaves fewer compute units idle. 256 x 256 has room for
+// two stages; the smaller tiles' steps wait longer for their copies, so those that
+// have room for three stages have them (515 tokens, 13824 x 5120: 192 x 192 54 ->
+// 48 us, 256 x 128 92 -> 84). Measured in a trace of 43 calls: 4096 tokens, 22016 x
+// 8192: 756 us (least 734: 2010 TFLOP/s) by rows, 743 (715: 2070) by columns. The
+// matrix unit is busy half of the cycles there, LDS a fifth, and the clock falls to
+// 1.8 - 1.9 GHz from the 2.35 of the 515 tokens' product.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 128;
 constexpr int kScales = 256 * 16;                     // four steps' token scales
@@ -396,7 +396,8 @@ __global__ __launch_bounds__(512, 2) void k_fp8_gemm(const uint8_t *__restrict__
 // float32 partial, and the last to arrive sums them in range order (so the
 // result does not depend on who is last) and writes the tile. Measured: 333
 // tokens, 5120 x 5120 by columns: 26 us; its copies alone take 19 of them, its
-// products alone as long (they share LDS), launch and sum 7.
+// products alone as long, launch and sum 7 (in a trace with the backward's other
+// launches around it: 28).
 // ---------------------------------------------------------------------------
 constexpr int kSmN = 128, kSmT = 64, kSmStages = 3;
 constexpr int kSmStage = (kSmN + kSmT) * kStep + kSmT * 4;  // weight tile, token tile, token scales
@@ -597,13 +598,15 @@ __global__ __launch_bounds__(256, 2) void k_fp8_gemm_small(const uint8_t *__rest
 // of a float32 and 48 bits that only this launch has (exchange.h). A reader whose
 // wait runs out (other launches hold the compute units) forms what it misses
 // itself, in the same order of operations, so no wait needs another workgroup to
-// run and the result does not depend on who formed what. Where the slices' partials are at most one
-// per thread of a reader (one token up to rank 64 of 4096 x 8192, four up to 16),
-// every reader takes and adds those instead, which spares the hop through the
-// last slice (1 token, 4096 x 4096: rank 16 8.6 -> 7.4 us, rank 64 9.3 -> 8.3). One compute unit reads about 28 GB/s from
-// memory, so a slice is kept to about 1024 of K (16 tokens, 4096 x 11008, r =
-// 64: 33.8 us with the whole of K in one workgroup, 19.8 with four slices,
-// 17.0 with eleven).
+// run and the result does not depend on who formed what.
+//
+// Where the slices' partials are at most one per thread of a reader (one token up
+// to rank 64 of 4096 x 8192, four up to 16), every reader takes and adds those
+// instead, which spares the hop through the last slice (1 token, 4096 x 4096: rank
+// 16 8.6 -> 7.1 us, rank 64 9.3 -> 8.3). One compute unit reads about 28 GB/s from
+// memory, so a slice is kept to about 1024 of K (16 tokens, 4096 x 11008, r = 64:
+// 33.8 us with the whole of K in one workgroup, 19.8 with four slices, 17.0 with
+// eleven; 18 since each value travels as a float32 instead of a bf16).
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8, kAhead = 4;
 constexpr int kUSlices = 16;  // at most
@@ -875,9 +878,11 @@ Fp8Plan fp8_plan(int64_t T, int64_t N, int64_t K, bool trans) {
   //   768 tokens  12288 x 8192              93  83 124 [78] 121
   //  1024 tokens  11008 x 4096             [54] 93  69  76   73
   //  4096 tokens   5120 x 5120             135 [116] 128 141 161
-  // and over 60 drawn shapes it stays within 2 % of the best on average. Large tiles: rounds of one workgroup per compute unit; where the last round
-  // would leave half of them idle, its tiles are cut into K ranges, whose partial tiles are written once more
-  // and read by one workgroup (45 bytes a ns).
+  // Over 80 drawn shapes of 17 tokens and more a call takes 3 % longer than with the best choice on average, 56 of
+  // them at most 2 %, and the worst 29 % (20 tokens, 3936 x 6656 by columns: nine K ranges, which are more workgroups
+  // than compute units, where eight take 15.3 us instead of 19.8).
+  // Large tiles: rounds of one workgroup per compute unit; where the last round would leave half of them idle, its tiles
+  // are cut into K ranges, whose partial tiles are written once more and read by one workgroup (45 bytes a ns).
   struct Large {
     int mi, mj;
     double step, ends;

@@ -6,12 +6,13 @@
 //
 // The bytes of P bound it: two read and one written per value. (Quantizer and
 // adapter product in launches of their own read P twice, and the adapter matrix
-// that is contracted over its other dimension was transposed first. 333 tokens, K = 5120, 16 ranks: 7.0 us, in three
-// launches 11.2; 4096 tokens, K = 8192: 23 us with 16 ranks, in three 36; 31 with 64, in three 36.)
+// that is contracted over its other dimension was transposed first. 333 tokens,
+// K = 5120, 16 ranks: 7.0 us, in three launches 11.2; 4096 tokens, K = 8192: 23 us
+// with 16 ranks, in three 36; 31 with 64, in three 36.)
 //
 // A workgroup owns 16 tokens per wave and a range of K, in steps of one scale
-// group (128). Tiles of P and Q are copied into LDS RS - 1 steps
-// ahead. A lane's fragments of a step are 32 consecutive values of one token
+// group (128). Tiles of P and Q are copied into LDS RS - 1 steps ahead. A lane's
+// fragments of a step are 32 consecutive values of one token
 // (4 x 8, the K of lane group g being 32 g .. 32 g + 31), so the group's maximum
 // takes two exchanges between lanes and the codes leave as whole 16 bytes; the
 // same registers are the second operand of the matrix instruction. The K ranges
