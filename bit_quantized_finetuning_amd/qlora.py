@@ -167,8 +167,12 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device index, as an integer
+
+
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The current stream of a tensor's device."""
+    return ctypes.c_void_p(_raw_stream(device.index))
 
 
 # ---------------------------------------------------------------------------
@@ -297,14 +301,34 @@ def _own_workspace(ws: torch.Tensor, nbytes: int) -> torch.Tensor:
     return ws
 
 
-@contextlib.contextmanager
-def _ws_for(ws, dev, nbytes: int):
-    """The caller's workspace, or the stream's cached one for as long as the call enqueues its launches."""
-    if ws is not None:
-        yield _own_workspace(ws, nbytes)
-        return
-    with _enqueue:
-        yield workspace(dev, nbytes)
+class _ws_for:
+    """The caller's workspace, or the stream's cached one, for as long as the call enqueues its launches."""
+    __slots__ = ("ws", "dev", "nbytes")
+
+    def __init__(self, ws, dev: torch.device, nbytes: int):
+        self.ws, self.dev, self.nbytes = ws, dev, nbytes
+
+    def __enter__(self) -> torch.Tensor:
+        if self.ws is not None:
+            return _own_workspace(self.ws, self.nbytes)
+        _enqueue.acquire()
+        try:
+            ws, index = None, self.dev.index
+            if self.dev.type == "cuda" and index == torch.cuda.current_device():
+                ws = _cached_ws(index, _raw_stream(index))
+            return workspace(self.dev, self.nbytes) if ws is None or ws.numel() < self.nbytes else ws
+        except BaseException:
+            _enqueue.release()
+            raise
+
+    def __exit__(self, *exc):
+        if self.ws is None:
+            _enqueue.release()
+
+
+def _cached_ws(dev: int, stream: int):
+    """The workspace cached for the current device's stream (None while a graph is captured, see workspace)."""
+    return None if torch.cuda.is_current_stream_capturing() else _workspaces.get(("cuda", dev, stream))
 
 
 def _bits(t: torch.Tensor) -> torch.Tensor:
@@ -736,19 +760,11 @@ def _groups(d: int) -> int:
     return -(-d // FP8_GROUP)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream of a device index, as an integer
-
-
 def _done(answer, where: str):
     """The results of a call that the native marshalling made; a status it got is raised."""
     if type(answer) is int:
         _check(answer, where)
     return answer
-
-
-def _cached_ws(dev: int, stream: int):
-    """The stream's cached workspace for a native call (None while a graph is captured, see workspace)."""
-    return None if torch.cuda.is_current_stream_capturing() else _workspaces.get(("cuda", dev, stream))
 
 
 def _on(dev):
