@@ -35,8 +35,11 @@
 namespace qlora {
 
 constexpr int kBwdThreads = 256, kBwdRows = 128, kBwdKeys = 128;
-// Rows that see at most so many keys have their delta corrected before dQ. The error that is left otherwise falls with the
-// root of their number (dQ's error over that of one rounding: 2.5 with 2 keys, 1.7 with 10, 1.3 with 64).
+// Rows that see at most so many keys (and those that share a wave with one) have their delta corrected before dQ. The error
+// that is left otherwise falls with the root of their number (dQ's error over that of one rounding: 2.5 with 2 keys, 1.7
+// with 10, 1.3 with 64; corrected 1.0). Time, with the pass and without: 2 x 2048 tokens, 40 over 8 heads, window 16, where
+// every row sees few, 111 and 95 us (reads from memory of tiles that are on their way into LDS as well); 8 x 512 tokens
+// without a window 167 and 166.
 constexpr int kFewKeys = 64;
 
 struct AttnGrad {
@@ -116,10 +119,12 @@ __global__ __launch_bounds__(kBwdThreads, 2) void k_attn_dq(AttnArgs a, AttnGrad
   const int64_t at = ((int64_t)b * a.H + head) * a.T + t;
   float rest = 0.f;  // this half's sum of P (dO V^T - delta)
   const float lse = p >= 0 ? gr.lse[at] : 0.f, lse2 = lse * 1.4426950408889634f;
-  // Of few keys that sum is no small part of dS: it is formed in a pass of its own, and corrects delta for dQ too.
-  if ((a.window < a.S ? a.window + a.sinks : a.S) <= kFewKeys) {
-    for (int i = 0; i < count; ++i) {
-      const int key0 = kts.key0(i, kKeys), key = key0 + ml;
+  // Of few keys that sum is no small part of dS: where the wave's first row sees few (a row at position p sees
+  // min(p + 1, window + sinks)), it is formed in a pass over the wave's own tiles, and corrects delta for dQ too.
+  if (q0 <= q1 && (q0 + 1 < a.window + a.sinks ? q0 + 1 : a.window + a.sinks) <= kFewKeys) {
+    const KeyTiles own = key_tiles(a, q0, q1, kKeys);
+    for (int i = 0; i < own.count; ++i) {
+      const int key0 = own.key0(i, kKeys), key = key0 + ml;
       u32x4 f[D / 16];
       f32x16 s = zero16(), dp = zero16();
       load_frags<D>(a.k.p + b * a.k.b + g * a.k.h + (int64_t)key * a.k.t, key < n, half, f);
