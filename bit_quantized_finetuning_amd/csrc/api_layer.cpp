@@ -45,14 +45,15 @@ int attention_args(const qlora_attention *p, AttnArgs &a) {
   return QLORA_OK;
 }
 
-// Rows of D values: 16-byte aligned, the rows of a head at least D values apart; offsets within 66 rows of the `rep`
-// heads of a group below 2^31 bytes.
-int attention_rows(const qlora_attention_rows &r, int64_t rows, int64_t D, int64_t rep, AttnRows &out) {
+// Rows of D values: 16-byte aligned, the rows of a head at least D values apart. The kernels add a lane's row of a tile of
+// 32 to the tile's address as a 32-bit byte offset: rows 2^24 values apart and more do not go. (Heads and sequences enter
+// the 64-bit address.)
+int attention_rows(const qlora_attention_rows &r, int64_t rows, int64_t D, AttnRows &out) {
   if (!r.p) return QLORA_ERR_NULL;
   constexpr int64_t kMost = (int64_t)1 << 40;
   const int64_t token = rows > 1 ? r.token : D;  // (the stride of a single row may be anything)
-  if (r.batch < 0 || r.batch > kMost || r.head < 0 || r.head > kMost || token < D || token > kMost) return QLORA_ERR_SHAPE;
-  if ((66 * token + rep * r.head + D) * 2 >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+  if (r.batch < 0 || r.batch > kMost || r.head < 0 || r.head > kMost || token < D || token >= QLORA_ATTENTION_MAX_STRIDE)
+    return QLORA_ERR_SHAPE;
   if (!aligned16(r.p) || r.batch % 8 || token % 8 || r.head % 8) return QLORA_ERR_ALIGN;
   out = AttnRows{r.p, r.batch, token, r.head};
   return QLORA_OK;
@@ -89,8 +90,8 @@ int qlora_attention_forward(const qlora_attention *p, const qlora_attention_rows
   int s = attention_args(p, a);
   if (s) return s;
   if (!q || !k || !v || !o) return QLORA_ERR_NULL;
-  if ((s = attention_rows(*q, p->T, p->D, a.rep, a.q)) || (s = attention_rows(*k, p->S, p->D, 1, a.k)) ||
-      (s = attention_rows(*v, p->S, p->D, 1, a.v)))
+  if ((s = attention_rows(*q, p->T, p->D, a.q)) || (s = attention_rows(*k, p->S, p->D, a.k)) ||
+      (s = attention_rows(*v, p->S, p->D, a.v)))
     return s;
   if (!aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3)) return QLORA_ERR_ALIGN;
   if (ws_bytes < qlora_attention_workspace_bytes(p->B, p->T, p->S, p->heads, p->kv_heads, p->D, p->window, p->sinks))
@@ -109,9 +110,9 @@ int qlora_attention_backward(const qlora_attention *p, const qlora_attention_row
   if (s) return s;
   if (!dO || !q || !k || !v || !o || !lse || !dq || !dk || !dv) return QLORA_ERR_NULL;
   AttnRows ro, rd;
-  if ((s = attention_rows(*q, p->T, p->D, a.rep, a.q)) || (s = attention_rows(*k, p->S, p->D, 1, a.k)) ||
-      (s = attention_rows(*v, p->S, p->D, 1, a.v)) || (s = attention_rows(*o, p->T, p->D, a.rep, ro)) ||
-      (s = attention_rows(*dO, p->T, p->D, a.rep, rd)))
+  if ((s = attention_rows(*q, p->T, p->D, a.q)) || (s = attention_rows(*k, p->S, p->D, a.k)) ||
+      (s = attention_rows(*v, p->S, p->D, a.v)) || (s = attention_rows(*o, p->T, p->D, ro)) ||
+      (s = attention_rows(*dO, p->T, p->D, rd)))
     return s;
   if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || (reinterpret_cast<uintptr_t>(lse) & 3)) return QLORA_ERR_ALIGN;
   if (ws_bytes <

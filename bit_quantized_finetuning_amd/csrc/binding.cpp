@@ -402,7 +402,8 @@ PyObject *rotary(PyObject *, PyObject *const *a, Py_ssize_t n) {
 qlora_attention_rows attention_rows(const Tensor &t, at::IntArrayRef shape) {
   need(t.defined() && t.scalar_type() == at::kBFloat16 && t.sizes() == shape && t.stride(3) == 1);
   const auto stride = [&](int i) { return t.size(i) > 1 ? t.stride(i) : 0; };
-  need(reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && (t.size(1) == 1 || stride(1) >= t.size(3)));
+  need(reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0);
+  need(t.size(1) == 1 || (stride(1) >= t.size(3) && stride(1) < QLORA_ATTENTION_MAX_STRIDE));
   for (int i = 0; i < 3; ++i) need(stride(i) % 8 == 0);
   return qlora_attention_rows{static_cast<const uint16_t *>(t.data_ptr()), stride(0), stride(1), stride(2)};
 }

@@ -185,7 +185,7 @@ def _attention_dense(t: torch.Tensor) -> torch.Tensor:
     """t [B, rows, heads, D] as the attention takes it (copied if its strides or alignment do not fit)."""
     strides = [s for n, s in zip(t.shape, t.stride()) if n > 1][:-1] if t.shape[3] > 1 else [1]
     fits = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in strides) and (
-        t.shape[1] <= 1 or t.stride(1) >= t.shape[3])
+        t.shape[1] <= 1 or t.shape[3] <= t.stride(1) < q.ATTENTION_MAX_STRIDE)
     return t if fits else t.clone(memory_format=torch.contiguous_format)
 
 

@@ -1351,6 +1351,7 @@ def qlora_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
 # ---------------------------------------------------------------------------
 
 NO_WINDOW = 1 << 30  # a window that hides nothing
+ATTENTION_MAX_STRIDE = 1 << 24  # QLORA_ATTENTION_MAX_STRIDE: the rows of a head are less than this apart
 
 
 def _attention_rows(t, name: str, shape):
@@ -1363,9 +1364,9 @@ def _attention_rows(t, name: str, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     strides = [s if n > 1 else 0 for n, s in zip(t.shape, t.stride())]
     if t.numel() and (t.stride(3) != 1 or t.data_ptr() % 16 or any(s % 8 for s in strides[:3]) or
-                      (t.shape[1] > 1 and strides[1] < t.shape[3])):
-        raise ValueError(f"{name}: the values of a head must be consecutive, its rows apart, everything aligned to 16 bytes, "
-                         f"got strides {t.stride()}")
+                      (t.shape[1] > 1 and not t.shape[3] <= strides[1] < ATTENTION_MAX_STRIDE)):
+        raise ValueError(f"{name}: the values of a head must be consecutive, its rows apart (by less than "
+                         f"{ATTENTION_MAX_STRIDE} values), everything aligned to 16 bytes, got strides {t.stride()}")
     return _AttentionRows(t.data_ptr(), *strides[:3])
 
 
@@ -1411,11 +1412,11 @@ def qlora_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, w
     """Causal attention with a sliding window and sinks: (o bf16 [B, T, heads, D], lse float32 [B, heads, T] | None).
 
     q [B, T, heads, D], k and v [B, S, kv_heads, D] (bf16, D 64 or 128, query head h over key head h // (heads / kv_heads);
-    any batch, token and head strides that are multiples of 8). The query at position p of a sequence of n keys sees the
-    keys j with j <= p, p < n and (p - j < window or j < sinks). lengths (int32 [B]): n, S without. offsets (int32 [B]): the
-    position of the first query, n - T without (the queries are the sequence's last: a decoded token against its cache);
-    a padded training batch has offsets of zeros. A query that sees nothing gives o = 0 and lse = -inf. scale: D^-1/2
-    unless given. Few queries are spread over the keys and joined within the launch."""
+    any batch, token and head strides that are multiples of 8, the token's below 2^24). The query at position p of a sequence
+    of n keys sees the keys j with j <= p, p < n and (p - j < window or j < sinks). lengths (int32 [B]): n, S without. offsets
+    (int32 [B]): the position of the first query, n - T without (the queries are the sequence's last: a decoded token against
+    its cache); a padded training batch has offsets of zeros. A query that sees nothing gives o = 0 and lse = -inf. scale:
+    D^-1/2 unless given. Few queries are spread over the keys and joined within the launch."""
     if _marshal is not None and ws is None and torch.is_tensor(q) and q.is_cuda:
         dev = torch.cuda.current_device()
         stream = _raw_stream(dev)

@@ -499,11 +499,12 @@ int qlora_rotary(const qlora_rotary_rows *rows, int32_t count, int dtype, int64_
  *   scale     > 0 and finite, also when multiplied by log2(e)
  *   heads     of queries, a multiple of kv_heads; query head h reads key head h / (heads / kv_heads);  D: 64 or 128
  * Rows are bf16 [B, T or S, heads or kv_heads, D], the D values consecutive, strides in elements (multiples of 8; the
- * rows of a head at least D apart). Products in bf16 with float32 sums; the softmax in float32, its weights rounded to
+ * rows of a head at least D and less than QLORA_ATTENTION_MAX_STRIDE apart; batch and head strides up to 2^40). Products in bf16 with float32 sums; the softmax in float32, its weights rounded to
  * bf16 for their product with v.
  * A value that is not finite reaches every query whose weight of it is not 0 by the mask, and, within 64 neighbouring
  * keys, may reach queries that do not see it.
  */
+#define QLORA_ATTENTION_MAX_STRIDE (1 << 24)
 typedef struct {
   int64_t B;
   int64_t T;

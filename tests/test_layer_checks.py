@@ -251,3 +251,24 @@ def test_attention_backward_scratch_is_bounded():
                                             (64, 512, 512, 32, 32, 128, 64, 1), (1, 1 << 20, 1 << 20, 8, 8, 128, 1, 128)):
         n = f(B, T, S, H, G, D, window, sinks)
         assert 32 * B * T * H <= n <= 32 * B * T * H + 512 * 2 * 128 * D * 4, (B, T, S, window, sinks, n)
+
+
+def test_attention_takes_heads_that_lie_far_apart():
+    """Heads in front of many tokens: only the rows of a head have to lie less than 2^24 values apart. (The workspace is too
+    small in every call, so that nothing is enqueued.)"""
+    T = 1 << 20
+    p = dict(B=1, T=T, S=T, heads=8, kv=1, D=128)
+    far = lambda: _rows(batch=8 * 128 * T, token=128, head=128 * T)  # noqa: E731
+    assert _af(p=_at(**p), rq=far(), rk=far(), rv=far(), n=0) == WORKSPACE
+    assert _ab(p=_at(**p), rd=far(), rq=far(), rk=far(), rv=far(), ro=far(), n=0) == WORKSPACE
+    assert _af(rq=_rows(head=1 << 40, batch=1 << 40), n=0) == WORKSPACE and _af(rq=_rows(head=1 << 41), n=0) == SHAPE
+    for call, names in ((_af, ("rq", "rk", "rv")), (_ab, ("rd", "rq", "rk", "rv", "ro"))):
+        for name in names:
+            assert call(**{name: _rows(token=(1 << 24) - 8)}, n=0) == WORKSPACE, name
+            assert call(**{name: _rows(token=1 << 24)}, n=0) == SHAPE, name
+    # (no memory behind it that a check could touch)
+    far = torch.empty(0, dtype=torch.bfloat16, device="meta").new_empty(2 * 3 << 24).as_strided((2, 3, 4, 64), (3 << 24, 1 << 24, 64, 1))
+    with pytest.raises(ValueError, match="strides"):
+        q._attention_rows(far, "q", (2, 3, 4, 64))
+    near = far.as_strided((2, 3, 4, 64), (3 << 24, (1 << 24) - 8, 64, 1))
+    assert q._attention_rows(near, "q", (2, 3, 4, 64)).token == (1 << 24) - 8
