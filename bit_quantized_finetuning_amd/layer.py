@@ -539,9 +539,11 @@ class QLoRAAttention(torch.nn.Module):
 class KeyValueCache:
     """The keys and values of `batch` sequences of up to `tokens` tokens, for inference.
 
-    k, v: [batch, tokens, kv_heads, head] (bf16); lengths: int32 [batch], on the device. `append` can be captured into a
-    graph: the lengths are read there on every replay. Only calls from the host are counted against `tokens`; what a replay
-    appends behind the last row is dropped."""
+    k, v: [batch, tokens, kv_heads, head] (bf16); lengths: int32 [batch], on the device. A sequence that would grow past
+    `tokens` is refused: `used` is the host's bound on the longest one (padded rows and all), and only where that bound does
+    not do, the lengths are read from the device. `append` can be captured into a graph: the lengths are read there on every
+    replay, what a replay appends behind the last row is dropped, and from then on calls outside of a graph ask the device
+    every time, which waits for it."""
 
     def __init__(self, batch: int, tokens: int, kv_heads: int, head: int, device="cuda"):
         if min(batch, tokens, kv_heads, head) < 1 or tokens >= q.MAX_TOKENS:
@@ -551,6 +553,7 @@ class KeyValueCache:
         self.k, self.v = self._kv[0, :, :tokens], self._kv[1, :, :tokens]
         self.lengths = torch.zeros(batch, dtype=torch.int32, device=device)
         self.tokens, self.used = tokens, 0
+        self._replays = False  # whether a graph may append too
 
     def reset(self):
         """Forget every sequence."""
@@ -570,9 +573,15 @@ class KeyValueCache:
                              f"{tuple(k.shape)} and {tuple(v.shape)}")
         if counts is not None and (counts.shape != self.lengths.shape or counts.dtype != torch.int32):
             raise ValueError("counts must be int32, one per sequence")
-        T = k.shape[1]
-        if self.used + T > self.tokens:
-            raise ValueError(f"{T} more tokens behind {self.used} in a cache of {self.tokens}")
+        T, used = k.shape[1], self.used
+        if self.lengths.is_cuda and torch.cuda.is_current_stream_capturing():  # nothing is appended yet
+            self._replays = True
+        else:
+            used = (int(self.lengths.max()) if self._replays else used) + T
+            if used > self.tokens:
+                used = int((self.lengths + (T if counts is None else counts.clamp(0, T))).max())
+            if used > self.tokens:
+                raise ValueError(f"{T} more tokens: sequences of up to {used} in a cache of {self.tokens}")
         before = self.lengths.clone()
         after = before + (T if counts is None else counts.clamp(0, T))
         at = self.positions(T)
@@ -581,5 +590,5 @@ class KeyValueCache:
         self._kv[0].index_put_((rows, at), k.to(torch.bfloat16))
         self._kv[1].index_put_((rows, at), v.to(torch.bfloat16))
         torch.clamp(after, max=self.tokens, out=self.lengths)
-        self.used += T
+        self.used = used
         return before

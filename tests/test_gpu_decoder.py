@@ -432,3 +432,39 @@ def test_training_moves_the_adapters():
         opt.step()
     torch.cuda.synchronize()
     assert all(not torch.equal(a, b) and torch.isfinite(b).all() for a, b in zip(before, params))
+
+
+def test_a_cache_that_replays_filled_refuses():
+    """After replays have filled a cache a call outside of the graph is refused instead of being dropped; with rows taken
+    back it lands behind what the replays appended."""
+    say("a cache after replays")
+    g = _gen("cache after replays")
+    c = L.KeyValueCache(2, 8, 1, 64)
+    t = _bf(g, 2, 1, 1, 64)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        c.append(t, t)
+    assert c.used == 0 and c.lengths.tolist() == [0, 0]
+    kept = []
+    for _ in range(6):
+        t.copy_(_bf(g, 2, 1, 1, 64))
+        kept.append(t.clone())
+        graph.replay()
+    c.append(t, t)
+    assert c.lengths.tolist() == [7, 7] and c.used == 7
+    graph.replay()
+    with pytest.raises(ValueError, match="8"):
+        c.append(t, t)
+    graph.replay()  # dropped
+    torch.cuda.synchronize()
+    want = torch.cat(kept + [t, t], 1)
+    assert torch.equal(c.k, want) and torch.equal(c.v, want) and c.lengths.tolist() == [8, 8]
+    c.lengths.copy_(_ints(2, 5))
+    new = _bf(g, 2, 3, 1, 64)
+    assert c.append(new, new).tolist() == [2, 5] and torch.equal(c.k[0, 2:5], new[0]) and torch.equal(c.k[1, 5:], new[1])
+    c.reset()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert c.lengths.tolist() == [1, 1] and torch.equal(c.k[:, :1], t)

@@ -72,3 +72,40 @@ def test_cache():
     assert c.lengths.tolist() == [10, 6, 9] and torch.equal(c.k[1, 3:6], k2[1]) and torch.equal(c.k[0, 7:], k2[0])
     c.reset()
     assert c.lengths.tolist() == [0, 0, 0] and c.used == 0
+
+
+def test_cache_counts_what_sequences_hold():
+    """A padded prompt that fills the cache's rows leaves the room behind each sequence; only what does not fit is refused,
+    and a refused call changes nothing."""
+    c = layer.KeyValueCache(2, 64, 1, 64, device="cpu")
+    g = torch.Generator().manual_seed(1)
+
+    def rows(T):
+        return torch.randn(2, T, 1, 64, generator=g).bfloat16()
+
+    k = rows(64)
+    c.append(k, k, torch.tensor([10, 7], dtype=torch.int32))
+    tokens = [rows(1) for _ in range(54)]
+    for t in tokens:
+        c.append(t, t)
+    assert c.lengths.tolist() == [64, 61] and c.used == 64
+    assert torch.equal(c.k[0], torch.cat([k[0, :10]] + [t[0] for t in tokens]))
+    assert torch.equal(c.v[1, :61], torch.cat([k[1, :7]] + [t[1] for t in tokens]))
+    before = c._kv.clone()
+    for n in (None, torch.tensor([1, 0], dtype=torch.int32), torch.tensor([0, 4], dtype=torch.int32)):
+        with pytest.raises(ValueError, match="64"):
+            c.append(rows(5), rows(5), n)
+    assert torch.equal(c._kv, before) and c.lengths.tolist() == [64, 61]
+    t = rows(5)  # no row of the longer one, three of the other's
+    assert c.append(t, t, torch.tensor([0, 3], dtype=torch.int32)).tolist() == [64, 61]
+    assert c.lengths.tolist() == [64, 64] and torch.equal(c.k[1, 61:], t[1, :3]) and torch.equal(c.k[0], before[0, 0, :64])
+    c.lengths.copy_(torch.tensor([3, 5]))  # tokens taken back
+    t = rows(59)
+    assert c.append(t, t).tolist() == [3, 5] and c.used == 64 and torch.equal(c.k[1, 5:], t[1])
+    t = rows(70)  # more rows than the cache has, few of them a sequence's
+    c.reset()
+    c.append(t, t, torch.tensor([64, 2], dtype=torch.int32))
+    assert c.lengths.tolist() == [64, 2] and torch.equal(c.k[0], t[0, :64]) and torch.equal(c.k[1, :2], t[1, :2])
+    c.reset()
+    with pytest.raises(ValueError):
+        c.append(t, t)
