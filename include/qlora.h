@@ -501,8 +501,9 @@ int qlora_rotary(const qlora_rotary_rows *rows, int32_t count, int dtype, int64_
  * Rows are bf16 [B, T or S, heads or kv_heads, D], the D values consecutive, strides in elements (multiples of 8; the
  * rows of a head at least D and less than QLORA_ATTENTION_MAX_STRIDE apart; batch and head strides up to 2^40). Products in bf16 with float32 sums; the softmax in float32, its weights rounded to
  * bf16 for their product with v.
- * A value that is not finite reaches every query whose weight of it is not 0 by the mask, and, within 64 neighbouring
- * keys, may reach queries that do not see it.
+ * A value that is not finite reaches what the formula gives it to. The products take tiles of 128 rows or keys whole, hidden
+ * pairs of query and key with a weight of 0: so one in v (of o), in k (of dq) or in q and dO (of dk and dv) may also reach
+ * the other side of a pair that the mask hides, where the key lies fewer than 160 positions from one that the query sees.
  */
 #define QLORA_ATTENTION_MAX_STRIDE (1 << 24)
 typedef struct {
