@@ -104,11 +104,11 @@ __device__ __forceinline__ void load_row(const AttnRows &x, int b, int t, int he
   for (int i = 0; i < D / 16; ++i) f[i] = ok ? ld16(p + 16 * i) : u32x4{0u, 0u, 0u, 0u};
 }
 
-// Output row and the logarithm of its sum. A row that sees nothing gives 0 and -inf.
+// Output row and the logarithm of its sum. A row that sees nothing (`some` false) gives 0 and -inf; one whose scores are all
+// -inf has a sum of 0 and gives NaN, as the formula does.
 template <int D>
 __device__ __forceinline__ void store_row(const AttnArgs &a, const AttnOut &out, int b, int t, int head, bool write,
-                                          bool seen, int half, float m, float l, f32x16 (&o)[D / 32]) {
-  const bool some = seen && l != 0.f;  // (a NaN sum stays)
+                                          bool some, int half, float m, float l, f32x16 (&o)[D / 32]) {
   const float inv = 1.f / l;
   uint16_t *row = out.o + (((int64_t)b * a.T + t) * a.H + head) * D;
 #pragma unroll
@@ -413,7 +413,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void k_attn_split(AttnArgs a, Att
   };
   if (splits == 1) {
     if (wave >= kDt) return;
-    const bool some = p >= 0 && l != 0.f;
+    const bool some = p >= 0;
     const float inv = 1.f / l;
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = some ? o[e] * inv : 0.f;
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(64 * kSplitWaves) void k_attn_split(AttnArgs a, Att
       sum += f * part_l[32 * s + tid];
       fac[32 * s + tid] = f;
     }
-    const bool some = p >= 0 && sum != 0.f;  // (tid < 32: this thread's own row)
+    const bool some = p >= 0;  // (tid < 32: this thread's own row)
     tot[tid] = some ? 1.f / sum : 0.f;
     if (out.lse) out.lse[((int64_t)b * a.H + head) * a.T + t] = final_lse(mx, sum, some);
   }
