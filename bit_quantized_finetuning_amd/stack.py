@@ -65,6 +65,8 @@ class DecoderProjections(torch.nn.Module):
             raise ValueError("gated is for the 4-bit base")
         if not attention and (window is not None or sinks):
             raise ValueError("window and sinks are for attention=True")
+        if attention and head not in (64, 128):
+            raise ValueError(f"attention has heads of 64 or 128 values, got {head}")
         self.base, self.attends, self.gated = base, bool(attention), gated
         self.hidden, self.kv, self.head = weights["q"].shape[0], weights["k"].shape[0], head
         if self.hidden % head or self.kv % head or self.hidden % self.kv:

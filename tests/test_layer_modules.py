@@ -109,3 +109,14 @@ def test_cache_counts_what_sequences_hold():
     c.reset()
     with pytest.raises(ValueError):
         c.append(t, t)
+
+
+def test_layers_refuse_heads_that_attention_has_not():
+    """At the construction, not in the first call; without attention any width goes on (here to the missing weights)."""
+    for head in (32, 96, 256):
+        with pytest.raises(ValueError, match="64 or 128"):
+            stack.DecoderProjections({}, head=head, attention=True)
+        with pytest.raises(KeyError):
+            stack.DecoderProjections({}, head=head)
+    with pytest.raises(KeyError):
+        stack.DecoderProjections({}, head=64, attention=True)
