@@ -3,6 +3,7 @@
 // before anything is enqueued, and the library allocates no memory.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -24,6 +25,9 @@ int attention_args(const qlora_attention *p, AttnArgs &a) {
   // indices of rows and of workgroups are 32-bit
   if (p->B > (1 << 24) || p->B * p->T * p->heads >= ((int64_t)1 << 31) || p->B * p->S * p->kv_heads >= ((int64_t)1 << 31))
     return QLORA_ERR_SHAPE;
+  // a launch takes fewer than 2^32 threads: workgroups of 256 for 128 rows, or keys, of a key head
+  const int64_t rows = std::max(p->T * (p->heads / p->kv_heads), p->S);
+  if (p->B * p->kv_heads * ((rows + 127) / 128) >= ((int64_t)1 << 24)) return QLORA_ERR_SHAPE;
   const float c = p->scale * 1.4426950408889634f;
   if (p->window < 1 || p->sinks < 0 || !(p->scale > 0.f) || !std::isfinite(c) || c < 1.1754944e-38f)
     return QLORA_ERR_VALUE;

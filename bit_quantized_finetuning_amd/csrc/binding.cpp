@@ -418,6 +418,7 @@ Attention attention(const Tensor &q, const Tensor &k, const Tensor &v, PyObject 
   need(B >= 1 && T >= 1 && S >= 1 && G >= 1 && H >= 1 && H <= QLORA_MAX_HEADS && H % G == 0 && (D == 64 || D == 128));
   need(T <= QLORA_MAX_TOKENS && S <= QLORA_MAX_TOKENS);
   need(B * T * H < ((int64_t)1 << 31) && B * S * G < ((int64_t)1 << 31));
+  need(B * G * ((std::max(T * (H / G), S) + 127) / 128) < ((int64_t)1 << 24));
   const int64_t w = as_int(window), s = as_int(sinks);
   const double f = scale == Py_None ? 1.0 / std::sqrt((double)D) : as_float(scale);
   need(w >= 1 && s >= 0 && f > 1e-30 && f < 1e30);

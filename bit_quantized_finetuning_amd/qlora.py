@@ -1390,7 +1390,8 @@ def _attention_args(q, k, v, window, sinks, scale, lengths, offsets):
         raise ValueError(f"heads of 64 or 128 values, got {D}")
     if not 1 <= H <= MAX_HEADS or G < 1 or H % G:
         raise ValueError(f"{H} query heads over {G} key heads: a multiple, at most {MAX_HEADS}")
-    if max(T, S) > MAX_TOKENS or B * T * H >= 1 << 31 or B * S * G >= 1 << 31:
+    if (max(T, S) > MAX_TOKENS or B * T * H >= 1 << 31 or B * S * G >= 1 << 31
+            or B * G * -(-max(T * H // G, S) // 128) >= 1 << 24):
         raise ValueError(f"too many rows: {B} x {T} x {H} queries, {B} x {S} x {G} keys")
     rows = [_attention_rows(q, "q", (B, T, H, D)), _attention_rows(k, "k", (B, S, G, D)),
             _attention_rows(v, "v", (B, S, G, D))]

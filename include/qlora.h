@@ -491,7 +491,8 @@ int qlora_rotary(const qlora_rotary_rows *rows, int32_t count, int dtype, int64_
  * position p of a sequence of n keys sees the keys j with j <= p, p < n and (p - j < window or j < sinks):
  *   o = softmax(scale q k^T over the keys it sees) v,   lse = log(sum exp(scale q k^T))
  * A query that sees nothing (its position negative, or n and past it) gives o = 0 and lse = -inf, and no gradient.
- *   B, T, S   sequences, queries of each, rows of each one's keys and values
+ *   B, T, S   sequences, queries of each, rows of each one's keys and values. T and S up to QLORA_MAX_TOKENS; B T heads and
+ *             B S kv_heads below 2^31; B kv_heads ceil(R / 128) below 2^24, R the larger of T heads / kv_heads and S
  *   lengths   device i32 [B], nullable: keys n of each sequence (taken as 0 .. S whatever they are), S without. Rows past n
  *             are not read, and get gradients of 0
  *   offsets   device i32 [B], nullable: position of each sequence's first query; n - T without (the queries are its last)

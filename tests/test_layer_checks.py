@@ -272,3 +272,19 @@ def test_attention_takes_heads_that_lie_far_apart():
         q._attention_rows(far, "q", (2, 3, 4, 64))
     near = far.as_strided((2, 3, 4, 64), (3 << 24, (1 << 24) - 8, 64, 1))
     assert q._attention_rows(near, "q", (2, 3, 4, 64)).token == (1 << 24) - 8
+
+
+def test_attention_refuses_more_workgroups_than_a_launch_takes():
+    """2^24 workgroups of 256 threads are one too many: refused as a shape, not by the launch. (Else the workspace is too
+    small, so that nothing is enqueued.)"""
+    most = 1 << 24
+    for sizes, err in ((dict(B=most, T=1, S=1, heads=1, kv=1), SHAPE), (dict(B=most - 1, T=1, S=1, heads=1, kv=1), WORKSPACE),
+                       (dict(B=most // 16, T=1, S=128, heads=16, kv=16), SHAPE),
+                       (dict(B=most // 16 - 1, T=1, S=128, heads=16, kv=16), WORKSPACE),
+                       (dict(B=most // 32, T=129, S=1, heads=16, kv=16), SHAPE), (dict(B=most // 32, T=33, S=1, heads=64, kv=16), SHAPE),
+                       (dict(B=most // 32, T=32, S=1, heads=64, kv=16), WORKSPACE)):
+        for call in (_af, _ab):
+            assert call(p=_at(**sizes), n=0) == err, sizes
+    x = torch.empty(0, dtype=torch.bfloat16, device="meta").new_empty(most, 1, 1, 64)
+    with pytest.raises(ValueError, match="too many"):
+        q.qlora_attention_forward(x, x, x)
