@@ -28,9 +28,8 @@ int attention_args(const qlora_attention *p, AttnArgs &a) {
   // a launch takes fewer than 2^32 threads: workgroups of 256 for 128 rows, or keys, of a key head
   const int64_t rows = std::max(p->T * (p->heads / p->kv_heads), p->S);
   if (p->B * p->kv_heads * ((rows + 127) / 128) >= ((int64_t)1 << 24)) return QLORA_ERR_SHAPE;
-  const float c = p->scale * 1.4426950408889634f;
-  if (p->window < 1 || p->sinks < 0 || !(p->scale > 0.f) || !std::isfinite(c) || c < 1.1754944e-38f)
-    return QLORA_ERR_VALUE;
+  // (the backward adds lse / scale to the scores: of less than 5e-38 that can pass float32's end)
+  if (p->window < 1 || p->sinks < 0 || !(p->scale > 1e-30f && p->scale < 1e30f)) return QLORA_ERR_VALUE;
   if ((p->lengths && (reinterpret_cast<uintptr_t>(p->lengths) & 3)) ||
       (p->offsets && (reinterpret_cast<uintptr_t>(p->offsets) & 3)))
     return QLORA_ERR_ALIGN;
@@ -45,7 +44,7 @@ int attention_args(const qlora_attention *p, AttnArgs &a) {
   a.window = p->window < (1 << 30) ? (int)p->window : 1 << 30;
   a.sinks = p->sinks < p->S ? (int)p->sinks : (int)p->S;
   a.scale = p->scale;
-  a.c = c;
+  a.c = p->scale * 1.4426950408889634f;
   return QLORA_OK;
 }
 

@@ -497,7 +497,7 @@ int qlora_rotary(const qlora_rotary_rows *rows, int32_t count, int dtype, int64_
  *             are not read, and get gradients of 0
  *   offsets   device i32 [B], nullable: position of each sequence's first query; n - T without (the queries are its last)
  *   window    >= 1 (any larger than S hides nothing);  sinks >= 0
- *   scale     > 0 and finite, also when multiplied by log2(e)
+ *   scale     between 1e-30 and 1e30
  *   heads     of queries, a multiple of kv_heads; query head h reads key head h / (heads / kv_heads);  D: 64 or 128
  * Rows are bf16 [B, T or S, heads or kv_heads, D], the D values consecutive, strides in elements (multiples of 8; the
  * rows of a head at least D and less than QLORA_ATTENTION_MAX_STRIDE apart; batch and head strides up to 2^40). Products in bf16 with float32 sums; the softmax in float32, its weights rounded to

@@ -288,3 +288,14 @@ def test_attention_refuses_more_workgroups_than_a_launch_takes():
     x = torch.empty(0, dtype=torch.bfloat16, device="meta").new_empty(most, 1, 1, 64)
     with pytest.raises(ValueError, match="too many"):
         q.qlora_attention_forward(x, x, x)
+
+
+def test_attention_scales_end_where_its_backward_does():
+    """lse of up to log(2^24) over the scale is added to the scores in float32: at 1e-38 that would be infinite. Every entry has
+    the binding's limits."""
+    for call in (_af, _ab):
+        for scale in (1e-38, 9e-39, 5e-38, 9e-31, 2e30, 1e38):
+            assert call(p=_at(scale=scale), n=0) == VALUE, scale
+        for scale in (2e-30, 1.0, 9e29):
+            assert call(p=_at(scale=scale), n=0) == WORKSPACE, scale
+    assert math.log(1 << 24) / 2e-30 < 3.4e38 < math.log(1 << 24) / 4e-38
