@@ -73,8 +73,8 @@ size_t qlora_attention_workspace_bytes(int64_t B, int64_t T, int64_t S, int32_t 
   if (B < 1 || T < 1 || S < 1 || T > kMaxTokens || S > kMaxTokens || heads < 1 || kv_heads < 1 || heads % kv_heads ||
       window < 1 || sinks < 0)
     return 0;
-  return kMaxCounters * 4 + 4 * attn_plan(B, T, S, heads, kv_heads, D, (int)clamped(window, 1 << 30),
-                                          (int)clamped(sinks, S)).partial_floats;
+  const size_t partial = attn_plan(B, T, S, heads, kv_heads, D, (int)clamped(window, 1 << 30), (int)clamped(sinks, S)).partial_floats;
+  return partial ? kExchangeEnd + 4 * partial : kMaxCounters * 4;
 }
 
 size_t qlora_attention_backward_workspace_bytes(int64_t B, int64_t T, int64_t S, int32_t heads, int32_t kv_heads,
@@ -101,7 +101,7 @@ int qlora_attention_forward(const qlora_attention *p, const qlora_attention_rows
     return QLORA_ERR_WORKSPACE;
   if (!ws) return QLORA_ERR_NULL;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
-  return hip_status(launch_attn_fwd(a, p->D, o, lse, at<float>(ws, kMaxCounters * 4), at<uint32_t>(ws, 0), stream));
+  return hip_status(launch_attn_fwd(a, p->D, o, lse, at<float>(ws, kExchangeEnd), at<uint32_t>(ws, 0), stream));
 }
 
 int qlora_attention_backward(const qlora_attention *p, const qlora_attention_rows *dO, const qlora_attention_rows *q,

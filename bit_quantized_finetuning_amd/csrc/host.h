@@ -13,6 +13,12 @@ namespace qlora {
 constexpr int64_t kMaxDim = QLORA_MAX_DIM;
 constexpr int64_t kMaxTokens = QLORA_MAX_TOKENS;
 
+// Behind the counters of a workspace lie the words that workgroups of one launch hand each other, known by a number that
+// they carry and not by a flag: at most the tagged partials of every job of a grouped forward at the largest rank. An
+// operator that runs between such launches keeps its scratch data behind them, since any of its values may look like the
+// next launch's number (the 4-bit base's is 32 bits).
+constexpr size_t kExchangeEnd = (size_t)kMaxCounters * 4 + (size_t)QLORA_MAX_FORWARD_JOBS * 4 * 16 * QLORA_MAX_RANK * 8;
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
