@@ -8,11 +8,11 @@
 // forward. delta from the bf16 O is off by O's rounding, which would be the
 // largest error after the results' own; a row's sum of P (dO V^T - delta),
 // which is 0 with the exact delta, says by how much, and the other kernel gets
-// the corrected one (dQ too where rows see few keys). dS enters dQ's product as two bf16 terms (the matrix unit
+// the corrected one (dQ too where rows see few keys, kFewKeys). dS enters dQ's product as two bf16 terms (the matrix unit
 // has room beside the LDS reads): without them dQ's error was 1.55 times that
 // of one rounding, with them 1.15 times; dK's is 1.43 times.
-// 2 x 4096 tokens, 40 over 8 heads, window 1024: 312 us, the matrix unit busy half of the cycles, as in the large products
-// over the base.
+// 2 x 4096 tokens, 40 over 8 heads, window 1024: 308 to 317 us, the matrix unit busy half of the cycles, as in the large
+// products over the base.
 //
 // k_attn_dkv: 128 keys of one key head per workgroup, 32 per wave, which holds
 // their K and V rows and both sums in registers (one wave per SIMD); the rows of
@@ -24,8 +24,9 @@
 // against ones: they arrive with the tile as 32 bytes a row that k_attn_dq left,
 // and cost a matrix instruction instead of LDS reads by every lane.
 // A step's 34 products (1088 cycles) and its 32 KB of LDS reads a wave (1024 cycles a CU) bound it together: 2 x 4096
-// tokens, 40 over 8 heads, window 1024, 454 us; without its copies 375, without LDS reads 410, without the sinks' shares
-// 420, the products alone about 280.
+// tokens, 40 over 8 heads, window 1024, 448 us; of an earlier form that took 454, without its copies 375, without LDS reads
+// 410, without the sinks' shares 420, the products alone about 280. Of a wave's time 57 % are an instruction's of its own,
+// 23 % it waits for its turn or a busy unit, 20 % for data.
 // The rows that only see the sinks would make the first key tile's list many
 // times as long as the others': they are shared out to workgroups of their own,
 // whose float32 sums k_attn_sinks adds, in order, to the first tiles'.
@@ -494,7 +495,8 @@ __global__ __launch_bounds__(kBwdThreads, 1) void k_attn_dkv(AttnArgs a, AttnGra
     int seen_head = 0, seen_cycle = (blocks - start) * a.rep, seen_left = count;  // tiles to the cycle's, to the list's end
     // The rows of a tile that see the key, as bits; each call is for the tile behind the last one's. Bits and two ANDs an
     // accumulator cost the same for every tile and hide behind the products; a branch around the masks of whole tiles
-    // made them wait for the scores (measured with the case below: 750 without masks, 800 with the branch).
+    // made them wait for the scores (an earlier form of this kernel, 2 x 4096 tokens as above: 750 us without any masks, 800
+    // with the branch).
     auto seen_rows = [&] {
       const auto from = [](int x) { return x > 31 ? 0u : 0xffffffffu << (x < 0 ? 0 : x); };
       const uint32_t m = (from(lo) & ~from(hi)) >> (4 * half);
@@ -677,7 +679,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_attn_sinks(AttnArgs a, AttnGrad
 }
 
 // The rows past the sink tiles' windows in about one share per compute unit, of 64 tokens at least (a share's waves
-// without sinks idle, and a workgroup has a unit to itself): 2 x 4096 tokens 467 us with them; a list of their own kept
+// without sinks idle, and a workgroup has a unit to itself): 2 x 4096 tokens 448 us with them; a list of their own kept
 // whole is four times as long as the others'. Where the sink tiles fill half of the units by themselves, or fewer than
 // kFarRows rows would be shared out (a step of 32 takes about 1 us, the second kernel 7), their lists stay whole.
 constexpr int kFarRows = 512;

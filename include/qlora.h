@@ -500,8 +500,8 @@ int qlora_rotary(const qlora_rotary_rows *rows, int32_t count, int dtype, int64_
  *   scale     between 1e-30 and 1e30
  *   heads     of queries, a multiple of kv_heads; query head h reads key head h / (heads / kv_heads);  D: 64 or 128
  * Rows are bf16 [B, T or S, heads or kv_heads, D], the D values consecutive, strides in elements (multiples of 8; the
- * rows of a head at least D and less than QLORA_ATTENTION_MAX_STRIDE apart; batch and head strides up to 2^40). Products in bf16 with float32 sums; the softmax in float32, its weights rounded to
- * bf16 for their product with v.
+ * rows of a head at least D and less than QLORA_ATTENTION_MAX_STRIDE apart; batch and head strides up to 2^40). Products in
+ * bf16 with float32 sums; the softmax in float32, its weights rounded to bf16 for their product with v.
  * A value that is not finite reaches what the formula gives it to. The products take tiles of 128 rows or keys whole, hidden
  * pairs of query and key with a weight of 0: so one in v (of o), in k (of dq) or in q and dO (of dk and dv) may also reach
  * the other side of a pair that the mask hides, where the key lies fewer than 160 positions from one that the query sees.
