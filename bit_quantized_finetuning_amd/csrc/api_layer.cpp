@@ -29,7 +29,7 @@ int attention_args(const qlora_attention *p, AttnArgs &a) {
   const int64_t rows = std::max(p->T * (p->heads / p->kv_heads), p->S);
   if (p->B * p->kv_heads * ((rows + 127) / 128) >= ((int64_t)1 << 24)) return QLORA_ERR_SHAPE;
   // (the backward adds lse / scale to the scores: of less than 5e-38 that can pass float32's end)
-  if (p->window < 1 || p->sinks < 0 || !(p->scale > 1e-30f && p->scale < 1e30f)) return QLORA_ERR_VALUE;
+  if (p->window < 1 || p->sinks < 0 || !(p->scale >= 1e-30f && p->scale <= 1e30f)) return QLORA_ERR_VALUE;
   if ((p->lengths && (reinterpret_cast<uintptr_t>(p->lengths) & 3)) ||
       (p->offsets && (reinterpret_cast<uintptr_t>(p->offsets) & 3)))
     return QLORA_ERR_ALIGN;

@@ -299,3 +299,11 @@ def test_attention_scales_end_where_its_backward_does():
         for scale in (2e-30, 1.0, 9e29):
             assert call(p=_at(scale=scale), n=0) == WORKSPACE, scale
     assert math.log(1 << 24) / 2e-30 < 3.4e38 < math.log(1 << 24) / 4e-38
+
+
+def test_scales_that_the_binding_takes_pass_the_entry_too():
+    """The binding compares in 64 bits, the entries the float32 that they get: one just above 1e-30 rounds to it."""
+    for scale in (1e-30 * (1 + 1e-12), 1e30 * (1 - 1e-12)):
+        assert 1e-30 < scale < 1e30
+        for call in (_af, _ab):
+            assert call(p=_at(scale=scale), n=0) == WORKSPACE, scale
